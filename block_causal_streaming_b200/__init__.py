@@ -36,7 +36,8 @@ _ABI_NAMES = (
     "qk_quantize_e4m3", "attn_forward_e4m3", "QkE4m3",
     "kv_append_publish_fp8", "kv_dequant_published", "Fp8Dst", "qk_i8_sizes", "qk_quantize_i8",
     "attn_forward_i8", "QkI8", "Segments", "attn_forward_segments",
-    "attn_segments_workspace_size",
+    "attn_segments_workspace_size", "WF_ERR_POSITION", "NormRope", "qk_norm_rope",
+    "kv_append_rope", "kv_append_fp8_block", "KvPoolFp8Block",
 )
 __all__ = list(_ABI_NAMES)
 

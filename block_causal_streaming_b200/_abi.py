@@ -22,6 +22,7 @@ WF_ERR_PAGE_OOB = 5
 WF_ERR_TIMEOUT = 6
 WF_ERR_CUDA = 7
 WF_ERR_NO_DEVICE = 8
+WF_ERR_POSITION = 9
 WF_MAX_CHUNKS = 64
 
 # Every symbol include/wf.h declares (checked by the CPU tests).
@@ -34,7 +35,8 @@ EXPORTED = ("wf_kv_append", "wf_attn_forward", "wf_check_status", "wf_strerror",
             "wf_attn_forward_e4m3", "wf_kv_append_publish_fp8", "wf_kv_dequant_published",
             "wf_qk_i8_sizes", "wf_qk_quantize_i8", "wf_attn_forward_i8",
             "wf_attn_forward_segments", "wf_attn_segments_workspace_size",
-            "wf_window_slots", "wf_window_round", "wf_window_round_ring")
+            "wf_window_slots", "wf_window_round", "wf_window_round_ring", "wf_qk_norm_rope",
+            "wf_kv_append_rope", "wf_kv_append_fp8_block")
 
 
 class WfError(RuntimeError):
@@ -81,6 +83,23 @@ class KvPoolFp8(ctypes.Structure):
                 ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
                 ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
                 ("num_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
+class KvPoolFp8Block(ctypes.Structure):
+    """wf_kv_pool_fp8_block_t: e4m3 codes [pages, page_size, H, D] and e8m0 scales
+    [pages, page_size / 16, H]."""
+    _fields_ = [("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("num_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
+class NormRopeC(ctypes.Structure):
+    """wf_norm_rope_t."""
+    _fields_ = [("norm", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("weight_per_head", ctypes.c_int32), ("cos_sin", ctypes.c_void_p),
+                ("table_rows", ctypes.c_int32), ("num_axes", ctypes.c_int32),
+                ("axis_pairs", ctypes.c_int32 * 3), ("interleaved", ctypes.c_int32)]
 
 
 class WindowC(ctypes.Structure):
@@ -229,6 +248,18 @@ def _load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.wf_attn_forward_segments.restype = i32
     lib.wf_attn_segments_workspace_size.argtypes = [ctypes.POINTER(SegmentsC), i32, i32, i32]
     lib.wf_attn_segments_workspace_size.restype = ctypes.c_size_t
+    i64 = ctypes.c_int64
+    lib.wf_qk_norm_rope.argtypes = [vp, i64, vp, vp, i32, vp, i64, vp, vp, i32, i32, i32, vp,
+                                    ctypes.POINTER(NormRopeC), vp]
+    lib.wf_qk_norm_rope.restype = i32
+    lib.wf_kv_append_rope.argtypes = [ctypes.POINTER(KvPool), i32, i32, i32, vp, i64, vp, i64, vp,
+                                      vp, ctypes.POINTER(NormRopeC), vp,
+                                      ctypes.POINTER(Wavefront), vp]
+    lib.wf_kv_append_rope.restype = i32
+    lib.wf_kv_append_fp8_block.argtypes = [ctypes.POINTER(KvPoolFp8Block), i32, i32, i32, vp, i64,
+                                           vp, i64, vp, vp, ctypes.POINTER(NormRopeC), vp,
+                                           ctypes.POINTER(Wavefront), vp]
+    lib.wf_kv_append_fp8_block.restype = i32
     return lib
 
 
@@ -893,6 +924,226 @@ def attn_forward_published(q, k_pool, v_pool, page_table_row, wf: WavefrontDesc,
         _stream_handle(stream))
     if rc != WF_OK:
         raise WfError(rc, "wf_attn_forward_published")
+
+
+# ---- norm and rotation of queries and keys, and the appends that carry them
+class NormRope:
+    """A wf_norm_rope_t: RMS norm of every (token, head) row and the rotation by position.
+
+    ``table``: fp32 [rows, pairs, 2] on the device (cos, sin of every position and pair, see
+    :func:`layer.rotation_table`), or None for no rotation; kept alive here.  ``axis_pairs``: pairs
+    that turn with each axis of the position (default: all with one axis)."""
+
+    def __init__(self, table=None, axis_pairs: Optional[Sequence[int]] = None,
+                 interleaved: bool = False, norm: bool = True, eps: float = 1e-6,
+                 weight_per_head: bool = False):
+        self.table, self.norm, self.weight_per_head = table, bool(norm), bool(weight_per_head)
+        self.num_axes = self.pairs = 0
+        rows = 0
+        if table is not None:
+            if table.dim() != 3 or table.shape[2] != 2:
+                raise ValueError(f"table: expected [rows, pairs, 2], got {tuple(table.shape)}")
+            _check_tensor(table, "table", "f32")
+            rows, self.pairs = int(table.shape[0]), int(table.shape[1])
+            axis_pairs = [self.pairs] if axis_pairs is None else [int(x) for x in axis_pairs]
+            if not 1 <= len(axis_pairs) <= 3 or sum(axis_pairs) != self.pairs or \
+                    min(axis_pairs) < 0:
+                raise ValueError(f"axis_pairs: 1 to 3 counts that sum to the table's {self.pairs} "
+                                 f"pairs, got {axis_pairs}")
+            self.num_axes = len(axis_pairs)
+        ap = (ctypes.c_int32 * 3)(*(list(axis_pairs) + [0, 0])[:3]) if table is not None else \
+            (ctypes.c_int32 * 3)()
+        self.c = NormRopeC(int(self.norm), float(eps), int(self.weight_per_head),
+                           table.data_ptr() if table is not None else None, rows, self.num_axes,
+                           ap, int(bool(interleaved)))
+        self.ref = ctypes.byref(self.c)
+
+
+def _check_cuda(t, name: str):
+    if not t.is_cuda:
+        raise ValueError(f"{name}: expected a CUDA tensor")
+
+
+def _check_one_device(stream, *tensors):
+    """Every tensor on the device the launch goes to: the current one."""
+    import torch
+    here = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != here:
+            raise ValueError(f"a tensor on {t.device}, the current device is {here}")
+
+
+def _rows_arg(t, name: str, L: int, H: int, D: int):
+    """(pointer, token stride) of a bf16 [L, H, D] tensor whose heads lie together."""
+    import torch
+    if tuple(t.shape) != (L, H, D):
+        raise ValueError(f"{name}: expected [{L}, {H}, {D}], got {tuple(t.shape)}")
+    if t.dtype is not torch.bfloat16:
+        raise TypeError(f"{name}: expected torch.bfloat16, got {t.dtype}")
+    _check_cuda(t, name)
+    s0, s1, s2 = t.stride()
+    if L * H * D == 0:
+        return None, H * D
+    if s2 != 1 or (H > 1 and s1 != D):
+        raise ValueError(f"{name}: every token's [{H}, {D}] must be contiguous, strides "
+                         f"{tuple(t.stride())}")
+    if L > 1 and (s0 < H * D or s0 % 8):
+        raise ValueError(f"{name}: the stride from token to token must be a multiple of 8 and at "
+                         f"least {H * D}, got {s0}")
+    return t.data_ptr(), s0 if L > 1 else H * D
+
+
+def _weight_arg(w, name: str, rule: Optional[NormRope], H: int, D: int):
+    if w is None:
+        return None
+    want = (H, D) if rule is not None and rule.weight_per_head else (D,)
+    if tuple(w.shape) != want:
+        raise ValueError(f"{name}: expected {list(want)}, got {tuple(w.shape)}")
+    if rule is None or not rule.norm:
+        raise ValueError(f"{name}: a weight without a norm")
+    _check_tensor(w, name, "bf16")
+    return w.data_ptr()
+
+
+def _positions_arg(positions, rule: Optional[NormRope], L: int, D: int):
+    if rule is None or rule.table is None:
+        if positions is not None:
+            raise ValueError("positions: the rule has no rotation")
+        return None
+    if rule.pairs * 2 > D:
+        raise ValueError(f"table: {rule.pairs} pairs in rows of {D} values")
+    if positions is None or tuple(positions.shape) != (L, rule.num_axes):
+        raise ValueError(f"positions: expected [{L}, {rule.num_axes}], got "
+                         f"{None if positions is None else tuple(positions.shape)}")
+    _check_tensor(positions, "positions", "i32")
+    return positions.data_ptr()
+
+
+def _overlap(a, b) -> bool:
+    """Whether two tensors' spans of memory meet."""
+    def span(t):
+        n = sum((int(x) - 1) * int(y) for x, y in zip(t.shape, t.stride())) + 1
+        return t.data_ptr(), t.data_ptr() + n * t.element_size()
+    if a.numel() == 0 or b.numel() == 0:
+        return False
+    (a0, a1), (b0, b1) = span(a), span(b)
+    return a0 < b1 and b0 < a1
+
+
+def qk_norm_rope(q, q_out, k, k_out, rule: NormRope, positions=None, q_weight=None,
+                 k_weight=None, stream=None) -> None:
+    """wf_qk_norm_rope: norm and rotation of ``q`` ([T, Hq, D] bf16, tokens may be strided) into
+    ``q_out`` and, in the same launch, of ``k`` into ``k_out`` (both None: queries only).
+    ``positions``: int32 [T, axes].  The outputs are contiguous; an output may be its own input."""
+    if q.dim() != 3:
+        raise ValueError(f"q: expected [T, H, D], got {tuple(q.shape)}")
+    L, Hq, D = (int(x) for x in q.shape)
+    qp, qs = _rows_arg(q, "q", L, Hq, D)
+    Hk, kp, ks, kop = 0, None, 0, None
+    if tuple(q_out.shape) != (L, Hq, D):
+        raise ValueError(f"q_out: expected [{L}, {Hq}, {D}], got {tuple(q_out.shape)}")
+    _check_tensor(q_out, "q_out", "bf16")
+    outs = [(q_out, "q_out", q)]
+    if (k is None) != (k_out is None):
+        raise ValueError("k and k_out go together")
+    if k is not None:
+        if k.dim() != 3:
+            raise ValueError(f"k: expected [T, H, D], got {tuple(k.shape)}")
+        Hk = int(k.shape[1])
+        kp, ks = _rows_arg(k, "k", L, Hk, D)
+        if tuple(k_out.shape) != (L, Hk, D):
+            raise ValueError(f"k_out: expected [{L}, {Hk}, {D}], got {tuple(k_out.shape)}")
+        _check_tensor(k_out, "k_out", "bf16")
+        kop = k_out.data_ptr()
+        outs.append((k_out, "k_out", k))
+        if _overlap(q_out, k_out):
+            raise ValueError("q_out and k_out overlap")
+    for o, n, own_in in outs:
+        for x in (q, k):
+            if x is None or (x is own_in and x.is_contiguous()):
+                continue
+            if _overlap(o, x) and not (x is own_in and x.data_ptr() == o.data_ptr() and
+                                       x.stride() == o.stride()):
+                raise ValueError(f"{n} overlaps an input (only its own, contiguous, may be the "
+                                 "same memory)")
+    qw = _weight_arg(q_weight, "q_weight", rule, Hq, D)
+    kw = _weight_arg(k_weight, "k_weight", rule, Hk, D)
+    pp = _positions_arg(positions, rule, L, D)
+    _check_one_device(stream, q, q_out, k, k_out, q_weight, k_weight, positions, rule.table)
+    rc = lib.wf_qk_norm_rope(qp, qs, q_out.data_ptr(), qw, Hq, kp, ks, kop, kw, Hk, L, D, pp,
+                             rule.ref, _stream_handle(stream))
+    if rc != WF_OK:
+        raise WfError(rc, "wf_qk_norm_rope")
+
+
+def _append_rows(k, v, chunk_begin: int, chunk_end: int, wf: WavefrontDesc, H: int, D: int):
+    """Pointers and strides of an append's rows, and their count."""
+    off = wf.chunk_offsets
+    if not 0 <= int(chunk_begin) < int(chunk_end) <= len(off) - 1:
+        raise ValueError(f"chunks [{chunk_begin}, {chunk_end}) outside the wavefront's "
+                         f"{len(off) - 1}")
+    L = off[chunk_end] - off[chunk_begin]
+    return (L,) + _rows_arg(k, "k", L, H, D) + _rows_arg(v, "v", L, H, D)
+
+
+def kv_append_rope(k_pool, v_pool, layer: int, chunk_begin: int, chunk_end: int, k, v, page_table,
+                   wf: WavefrontDesc, rule: NormRope, positions=None, k_weight=None,
+                   stream=None) -> None:
+    """wf_kv_append_rope: chunks [chunk_begin, chunk_end) into the bf16 pools, keys normed and
+    rotated on the way.  ``k``, ``v``: those chunks' rows, [L, H, D] bf16, tokens may be strided."""
+    num_pages, page_size, H, D = _pool_shape(k_pool, v_pool)
+    L, kp, ks, vp, vs = _append_rows(k, v, chunk_begin, chunk_end, wf, H, D)
+    _check_page_table(page_table, layer, wf)
+    _check_tensor(k_pool, "k_pool", "bf16")
+    _check_tensor(v_pool, "v_pool", "bf16")
+    _check_tensor(page_table, "page_table", "i32")
+    kw = _weight_arg(k_weight, "k_weight", rule, H, D)
+    pp = _positions_arg(positions, rule, L, D)
+    _check_one_device(stream, k_pool, v_pool, k, v, page_table, k_weight, positions, rule.table)
+    pool = KvPool(k_pool.data_ptr(), v_pool.data_ptr(), num_pages, page_size, H, D)
+    rc = lib.wf_kv_append_rope(ctypes.byref(pool), int(layer), int(chunk_begin), int(chunk_end),
+                               kp, ks, vp, vs, kw, pp, rule.ref, page_table.data_ptr(),
+                               ctypes.byref(wf.c), _stream_handle(stream))
+    if rc != WF_OK:
+        raise WfError(rc, "wf_kv_append_rope")
+
+
+def _fp8_block_pool(k_codes, v_codes, k_scale, v_scale) -> KvPoolFp8Block:
+    num_pages, page_size, H, D = _pool_shape(k_codes, v_codes, "FP8 cache codes")
+    want = (num_pages, page_size // 16, H)
+    if tuple(k_scale.shape) != want or tuple(v_scale.shape) != want:
+        raise ValueError(f"FP8 cache: scales must be {list(want)} (pages, page_size / 16, H), got "
+                         f"{tuple(k_scale.shape)} and {tuple(v_scale.shape)}")
+    for t, n in ((k_codes, "k_codes"), (v_codes, "v_codes"), (k_scale, "k_scale"),
+                 (v_scale, "v_scale")):
+        _check_tensor(t, n, "u8")
+    return KvPoolFp8Block(k_codes.data_ptr(), v_codes.data_ptr(), k_scale.data_ptr(),
+                          v_scale.data_ptr(), num_pages, page_size, H, D)
+
+
+def kv_append_fp8_block(k_codes, v_codes, k_scale, v_scale, layer: int, chunk_begin: int,
+                        chunk_end: int, k, v, page_table, wf: WavefrontDesc,
+                        rule: Optional[NormRope] = None, positions=None, k_weight=None,
+                        stream=None) -> None:
+    """wf_kv_append_fp8_block: chunks [chunk_begin, chunk_end) into an FP8 cache (uint8 e4m3 codes
+    [pages, page_size, H, D], uint8 e8m0 scales [pages, page_size / 16, H]; zeroed at first), keys
+    normed and rotated on the way when ``rule`` is given."""
+    pool = _fp8_block_pool(k_codes, v_codes, k_scale, v_scale)
+    H, D = pool.num_heads, pool.head_dim
+    L, kp, ks, vp, vs = _append_rows(k, v, chunk_begin, chunk_end, wf, H, D)
+    _check_page_table(page_table, layer, wf)
+    _check_tensor(page_table, "page_table", "i32")
+    kw = _weight_arg(k_weight, "k_weight", rule, H, D)
+    pp = _positions_arg(positions, rule, L, D)
+    _check_one_device(stream, k_codes, v_codes, k_scale, v_scale, k, v, page_table, k_weight,
+                      positions, rule.table if rule is not None else None)
+    rc = lib.wf_kv_append_fp8_block(ctypes.byref(pool), int(layer), int(chunk_begin),
+                                    int(chunk_end), kp, ks, vp, vs, kw, pp,
+                                    rule.ref if rule is not None else None,
+                                    page_table.data_ptr(), ctypes.byref(wf.c),
+                                    _stream_handle(stream))
+    if rc != WF_OK:
+        raise WfError(rc, "wf_kv_append_fp8_block")
 
 
 def ipc_export(device_ptr: int):

@@ -17,6 +17,7 @@
 #include "append_kernel.cuh"
 #include "attn_kernel.cuh"
 #include "combine_kernel.cuh"
+#include "fp8_block_kernel.cuh"
 #include "fp8_kernel.cuh"
 #include "i8_kernel.cuh"
 #include "publish_kernel.cuh"
@@ -594,6 +595,7 @@ const char* wf_strerror(int code) {
     case WF_ERR_TIMEOUT: return "WF_ERR_TIMEOUT: a bounded wait inside a kernel ran out";
     case WF_ERR_CUDA: return "WF_ERR_CUDA: a CUDA call failed";
     case WF_ERR_NO_DEVICE: return "WF_ERR_NO_DEVICE: no sm_100 device is current";
+    case WF_ERR_POSITION: return "WF_ERR_POSITION: a position is outside the rotation table";
     default: return "unknown wf error code";
   }
 }
@@ -1353,6 +1355,250 @@ int wf_check_status(wf_stream_t stream) {
     return WF_ERR_CUDA;
   }
   return st;
+}
+
+}  // extern "C"
+
+// ------------------------------------------------ norm and rotation, appends that carry them
+namespace {
+
+// Checks a rule (null: neither norm nor rotation) and fills the kernels' form of it.
+int norm_rope_rule(const wf_norm_rope_t* rule, const int32_t* positions, int D,
+                   wfk::NormRope* out, wfk::RopeMode* mode) {
+  std::memset(out, 0, sizeof(*out));
+  *mode = wfk::kRopeNone;
+  if (rule == nullptr) return WF_OK;
+  if (rule->norm != 0 && rule->norm != 1) return WF_ERR_INVALID_ARG;
+  if (rule->weight_per_head != 0 && rule->weight_per_head != 1) return WF_ERR_INVALID_ARG;
+  if (!(rule->eps >= 0.f) || !std::isfinite(rule->eps)) return WF_ERR_INVALID_ARG;
+  out->norm = rule->norm;
+  out->eps = rule->eps;
+  if (rule->cos_sin == nullptr) return WF_OK;
+  if (!aligned16(rule->cos_sin) || positions == nullptr ||
+      (reinterpret_cast<uintptr_t>(positions) & 3u) ||
+      (rule->interleaved != 0 && rule->interleaved != 1))
+    return WF_ERR_INVALID_ARG;
+  if (rule->table_rows < 1 || rule->num_axes < 1 || rule->num_axes > 3) return WF_ERR_SHAPE;
+  int64_t pairs = 0;
+  int64_t first[3] = {0, 0, 0};
+  for (int i = 0; i < rule->num_axes; ++i) {
+    if (rule->axis_pairs[i] < 0) return WF_ERR_SHAPE;
+    first[i] = pairs;
+    pairs += rule->axis_pairs[i];
+  }
+  if (pairs < 4 || pairs > D / 2 || pairs % 4 != 0) return WF_ERR_SHAPE;
+  out->table = reinterpret_cast<const float2*>(rule->cos_sin);
+  out->positions = positions;
+  out->table_rows = rule->table_rows;
+  out->pairs = static_cast<int>(pairs);
+  out->num_axes = rule->num_axes;
+  out->axis1 = static_cast<int>(rule->num_axes > 1 ? first[1] : pairs);
+  out->axis2 = static_cast<int>(rule->num_axes > 2 ? first[2] : pairs);
+  *mode = rule->interleaved ? wfk::kRopeInterleaved
+          : 2 * pairs == D  ? wfk::kRopeSplit
+                            : wfk::kRopeSplitPartial;
+  return WF_OK;
+}
+
+bool weight_ok(const void* w) { return (reinterpret_cast<uintptr_t>(w) & 7u) == 0; }
+
+// A tensor of `tokens` rows of heads x D values, `stride` values apart (unused for one row).
+bool rows_ok(const void* p, int64_t stride, int heads, int D, int tokens) {
+  return p != nullptr && aligned16(p) &&
+         (tokens <= 1 || (stride >= static_cast<int64_t>(heads) * D && stride % 8 == 0));
+}
+
+int block_count(const DeviceState* d, int64_t items, int per_sm) {
+  const int64_t per_block = wfk::kNormRopeThreads / 32;
+  const int64_t blocks = (items + per_block - 1) / per_block;
+  return static_cast<int>(std::min<int64_t>(blocks, static_cast<int64_t>(d->num_sms) * per_sm));
+}
+
+// Splits each token's rows into work items and launches.
+template <bool kAppend>
+int launch_norm_rope(wfk::NormRopeParams* p, wfk::RopeMode mode, int D, const DeviceState* d,
+                     cudaStream_t s) {
+  const int rows = p->set[0].heads + p->set[1].heads;
+  const int rps = 256 / D;                         // rows a warp covers in one step
+  const int steps = (rows + rps - 1) / rps;
+  const int64_t want = static_cast<int64_t>(d->num_sms) * 48;      // warps that fill the GPU
+  int per_token = static_cast<int>(std::min<int64_t>((want + p->tokens - 1) / p->tokens, steps));
+  p->chunk = (steps + per_token - 1) / per_token * rps;
+  p->items_per_token = (rows + p->chunk - 1) / p->chunk;
+  const int blocks = block_count(d, static_cast<int64_t>(p->tokens) * p->items_per_token, 16);
+  const int th = wfk::kNormRopeThreads;
+#define WF_LAUNCH(D_, M_) wfk::wf_norm_rope_kernel<D_, M_, kAppend><<<blocks, th, 0, s>>>(*p)
+  if (D == 128) {
+    if (mode == wfk::kRopeNone) WF_LAUNCH(128, wfk::kRopeNone);
+    else if (mode == wfk::kRopeInterleaved) WF_LAUNCH(128, wfk::kRopeInterleaved);
+    else if (mode == wfk::kRopeSplit) WF_LAUNCH(128, wfk::kRopeSplit);
+    else WF_LAUNCH(128, wfk::kRopeSplitPartial);
+  } else {
+    if (mode == wfk::kRopeNone) WF_LAUNCH(64, wfk::kRopeNone);
+    else if (mode == wfk::kRopeInterleaved) WF_LAUNCH(64, wfk::kRopeInterleaved);
+    else if (mode == wfk::kRopeSplit) WF_LAUNCH(64, wfk::kRopeSplit);
+    else WF_LAUNCH(64, wfk::kRopeSplitPartial);
+  }
+#undef WF_LAUNCH
+  return cudaGetLastError() == cudaSuccess ? WF_OK : WF_ERR_CUDA;
+}
+
+// The token range of chunks [chunk_begin, chunk_end) and the checks the two appends share, after
+// the pool's own (geo: the pool's geometry).
+int append_range(const wf_kv_pool_t* geo, int layer, int chunk_begin, int chunk_end,
+                 const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                 const void* k_weight, const int32_t* page_table, const wf_wavefront_t* wf,
+                 int* t0, int* rows, int* live) {
+  int rc = validate_wavefront(wf, geo, live);
+  if (rc) return rc;
+  if (layer < 0 || chunk_begin < 0 || chunk_end <= chunk_begin || chunk_end > wf->num_chunks ||
+      page_table == nullptr || (reinterpret_cast<uintptr_t>(page_table) & 3u))
+    return WF_ERR_INVALID_ARG;
+  *t0 = wf->chunk_offsets[chunk_begin];
+  *rows = wf->chunk_offsets[chunk_end] - *t0;
+  if (*rows == 0) return WF_OK;
+  if (!rows_ok(k, k_stride, geo->num_heads, geo->head_dim, *rows) ||
+      !rows_ok(v, v_stride, geo->num_heads, geo->head_dim, *rows) || !weight_ok(k_weight))
+    return WF_ERR_INVALID_ARG;
+  return WF_OK;
+}
+
+int validate_pool_fp8_block(const wf_kv_pool_fp8_block_t* pool) {
+  if (pool == nullptr || pool->k_codes == nullptr || pool->v_codes == nullptr ||
+      pool->k_scale == nullptr || pool->v_scale == nullptr)
+    return WF_ERR_INVALID_ARG;
+  const wf_kv_pool_t g{pool->k_codes, pool->v_codes, pool->num_pages, pool->page_size,
+                       pool->num_heads, pool->head_dim};
+  return validate_pool(&g);
+}
+
+}  // namespace
+
+extern "C" {
+
+int wf_qk_norm_rope(const void* q, int64_t q_stride, void* q_out, const void* q_weight,
+                    int num_q_heads, const void* k, int64_t k_stride, void* k_out,
+                    const void* k_weight, int num_k_heads, int tokens, int head_dim,
+                    const int32_t* positions, const wf_norm_rope_t* rule, wf_stream_t stream) {
+  if (head_dim != 64 && head_dim != 128) return WF_ERR_SHAPE;
+  if (num_q_heads < 1 || num_k_heads < 0 || tokens < 0 ||
+      static_cast<int64_t>(num_q_heads) + num_k_heads > INT32_MAX / 256)
+    return WF_ERR_SHAPE;
+  if (rule == nullptr) return WF_ERR_INVALID_ARG;
+  wfk::NormRopeParams p;
+  std::memset(&p, 0, sizeof(p));
+  wfk::RopeMode mode;
+  if (tokens == 0) return WF_OK;
+  int rc = norm_rope_rule(rule, positions, head_dim, &p.rule, &mode);
+  if (rc) return rc;
+  if (!rows_ok(q, q_stride, num_q_heads, head_dim, tokens) || q_out == nullptr ||
+      !aligned16(q_out) || !weight_ok(q_weight))
+    return WF_ERR_INVALID_ARG;
+  if (num_k_heads > 0 && (!rows_ok(k, k_stride, num_k_heads, head_dim, tokens) ||
+                          k_out == nullptr || !aligned16(k_out) || !weight_ok(k_weight)))
+    return WF_ERR_INVALID_ARG;
+  DeviceState* d = nullptr;
+  rc = device_state(&d);
+  if (rc) return rc;
+  using bf16 = __nv_bfloat16;
+  p.set[0] = {static_cast<const bf16*>(q), q_stride, static_cast<bf16*>(q_out),
+              static_cast<const bf16*>(q_weight), num_q_heads};
+  p.set[1] = {static_cast<const bf16*>(k), k_stride, static_cast<bf16*>(k_out),
+              static_cast<const bf16*>(k_weight), num_k_heads};
+  p.weight_per_head = rule->weight_per_head;
+  p.tokens = tokens;
+  p.status = d->status;
+  return launch_norm_rope<false>(&p, mode, head_dim, d, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int wf_kv_append_rope(const wf_kv_pool_t* pool, int layer, int chunk_begin, int chunk_end,
+                      const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                      const void* k_weight, const int32_t* positions, const wf_norm_rope_t* rule,
+                      const int32_t* page_table, const wf_wavefront_t* wf, wf_stream_t stream) {
+  int rc = validate_pool(pool);
+  if (rc) return rc;
+  if (rule == nullptr) return WF_ERR_INVALID_ARG;
+  int t0 = 0, rows = 0, live = 0;
+  rc = append_range(pool, layer, chunk_begin, chunk_end, k, k_stride, v, v_stride, k_weight,
+                    page_table, wf, &t0, &rows, &live);
+  if (rc || rows == 0) return rc;
+  wfk::NormRopeParams p;
+  std::memset(&p, 0, sizeof(p));
+  wfk::RopeMode mode;
+  rc = norm_rope_rule(rule, positions, pool->head_dim, &p.rule, &mode);
+  if (rc) return rc;
+  DeviceState* d = nullptr;
+  rc = device_state(&d);
+  if (rc) return rc;
+  using bf16 = __nv_bfloat16;
+  p.set[0] = {static_cast<const bf16*>(k), k_stride, static_cast<bf16*>(pool->k_pool),
+              static_cast<const bf16*>(k_weight), pool->num_heads};
+  p.set[1] = {static_cast<const bf16*>(v), v_stride, static_cast<bf16*>(pool->v_pool), nullptr,
+              pool->num_heads};
+  p.weight_per_head = rule->weight_per_head;
+  p.tokens = rows;
+  p.status = d->status;
+  p.pt_row = page_table + static_cast<int64_t>(layer) * wf->max_pages_per_seq;
+  p.token0 = t0;
+  p.page_size = pool->page_size;
+  p.num_pages = pool->num_pages;
+  return launch_norm_rope<true>(&p, mode, pool->head_dim, d,
+                                reinterpret_cast<cudaStream_t>(stream));
+}
+
+int wf_kv_append_fp8_block(const wf_kv_pool_fp8_block_t* pool, int layer, int chunk_begin,
+                           int chunk_end, const void* k, int64_t k_stride, const void* v,
+                           int64_t v_stride, const void* k_weight, const int32_t* positions,
+                           const wf_norm_rope_t* rule, const int32_t* page_table,
+                           const wf_wavefront_t* wf, wf_stream_t stream) {
+  int rc = validate_pool_fp8_block(pool);
+  if (rc) return rc;
+  const wf_kv_pool_t geo{pool->k_codes, pool->v_codes, pool->num_pages, pool->page_size,
+                         pool->num_heads, pool->head_dim};
+  wfk::Fp8BlockAppendParams p;
+  std::memset(&p, 0, sizeof(p));
+  rc = append_range(&geo, layer, chunk_begin, chunk_end, k, k_stride, v, v_stride, k_weight,
+                    page_table, wf, &p.token0, &p.tokens, &p.live);
+  if (rc || p.tokens == 0) return rc;
+  wfk::RopeMode mode;
+  rc = norm_rope_rule(rule, positions, pool->head_dim, &p.rule, &mode);
+  if (rc) return rc;
+  DeviceState* d = nullptr;
+  rc = device_state(&d);
+  if (rc) return rc;
+  using bf16 = __nv_bfloat16;
+  p.set[0] = {static_cast<const bf16*>(k), k_stride, nullptr, static_cast<const bf16*>(k_weight),
+              pool->num_heads};
+  p.set[1] = {static_cast<const bf16*>(v), v_stride, nullptr, nullptr, pool->num_heads};
+  p.codes[0] = static_cast<uint8_t*>(pool->k_codes);
+  p.codes[1] = static_cast<uint8_t*>(pool->v_codes);
+  p.scale[0] = static_cast<uint8_t*>(pool->k_scale);
+  p.scale[1] = static_cast<uint8_t*>(pool->v_scale);
+  p.weight_per_head = rule != nullptr ? rule->weight_per_head : 0;
+  p.H = pool->num_heads;
+  p.page_size = pool->page_size;
+  p.num_pages = pool->num_pages;
+  p.pt_row = page_table + static_cast<int64_t>(layer) * wf->max_pages_per_seq;
+  p.status = d->status;
+  const int64_t nb = (p.token0 + int64_t{p.tokens} - 1) / wfk::kFp8BlockTokens -
+                     p.token0 / wfk::kFp8BlockTokens + 1;
+  const int blocks = block_count(d, nb * 2 * p.H, 16);
+  const int th = wfk::kNormRopeThreads;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+#define WF_LAUNCH(D_, M_) wfk::wf_fp8_block_append_kernel<D_, M_><<<blocks, th, 0, s>>>(p)
+  if (pool->head_dim == 128) {
+    if (mode == wfk::kRopeNone) WF_LAUNCH(128, wfk::kRopeNone);
+    else if (mode == wfk::kRopeInterleaved) WF_LAUNCH(128, wfk::kRopeInterleaved);
+    else if (mode == wfk::kRopeSplit) WF_LAUNCH(128, wfk::kRopeSplit);
+    else WF_LAUNCH(128, wfk::kRopeSplitPartial);
+  } else {
+    if (mode == wfk::kRopeNone) WF_LAUNCH(64, wfk::kRopeNone);
+    else if (mode == wfk::kRopeInterleaved) WF_LAUNCH(64, wfk::kRopeInterleaved);
+    else if (mode == wfk::kRopeSplit) WF_LAUNCH(64, wfk::kRopeSplit);
+    else WF_LAUNCH(64, wfk::kRopeSplitPartial);
+  }
+#undef WF_LAUNCH
+  return cudaGetLastError() == cudaSuccess ? WF_OK : WF_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -59,7 +59,9 @@ enum {
                               written (append) or was read as page 0 (attention) */
   WF_ERR_TIMEOUT = 6,      /* device: a bounded wait inside a kernel ran out; the kernel stopped */
   WF_ERR_CUDA = 7,         /* a CUDA runtime or driver call failed */
-  WF_ERR_NO_DEVICE = 8     /* no sm_100 device is current */
+  WF_ERR_NO_DEVICE = 8,    /* no sm_100 device is current */
+  WF_ERR_POSITION = 9      /* device: a position outside the rotation table; that token was not
+                              written */
 };
 
 /* Maximum number of chunks (context + active) in one wavefront descriptor. */
@@ -466,6 +468,103 @@ int wf_qk_quantize_e4m3(const void* q, const wf_kv_pool_t* kv_pages,
 int wf_attn_forward_e4m3(const wf_qk_e4m3_t* qk, const wf_kv_pool_t* kv_pages,
                          const int32_t* page_table_row, const wf_wavefront_t* wf, float scale,
                          void* out, float* lse_or_null, wf_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * From the QKV projection to the cache: norms of queries and keys for each head with the position
+ * rotation in the same pass (the step of a DiT layer between the projection and the publication
+ * of K/V, KipQuest "The deep dive"; the pages give no formula, so it is the usual one).
+ *
+ * For one (token, head) row x of D values:
+ *   y = x / sqrt(mean(x^2) + eps) * weight      (norm = 1; y = x with norm = 0)
+ *   pair i turns by its angle:  (y_a, y_b) <- (y_a cos - y_b sin, y_a sin + y_b cos)
+ * in fp32 throughout, rounded once.  Pairs are (2i, 2i + 1) with interleaved = 1, (i, pairs + i)
+ * with 0; channels from 2 pairs on are not turned.  cos and sin are read from `cos_sin` at row
+ * positions[token][axis of the pair]: the first axis_pairs[0] pairs turn with axis 0, the next
+ * axis_pairs[1] with axis 1, and so on (one axis for a sequence; frame, row and column for video).
+ */
+typedef struct {
+  int32_t norm;             /* 1: RMS norm of every (token, head) row; 0: none (weights unused) */
+  float eps;                /* >= 0, finite */
+  int32_t weight_per_head;  /* 0: weights are [D]; 1: [H][D] */
+  const float* cos_sin;     /* device fp32 [table_rows][pairs][2] (cos, sin), 16-byte aligned;
+                               NULL: no rotation, the fields below are unused */
+  int32_t table_rows;       /* positions are in [0, table_rows) */
+  int32_t num_axes;         /* 1..3 */
+  int32_t axis_pairs[3];    /* pairs of each axis, >= 0; their sum, `pairs`, is a multiple of 4 in
+                               4..D/2 */
+  int32_t interleaved;
+} wf_norm_rope_t;
+
+/*
+ * wf_qk_norm_rope -- norm and rotation of queries and, in the same launch, keys.
+ *
+ *   q, k           device bf16 rows [num_q_heads][D] / [num_k_heads][D] for each token, q_stride /
+ *                  k_stride values from token to token (>= heads x D, a multiple of 8), 16-byte
+ *                  aligned: contiguous tensors or slices of a fused projection's output.
+ *   q_out, k_out   device bf16 [tokens][heads][D], contiguous, 16-byte aligned.  May be the input
+ *                  itself where that is contiguous; no other overlap.
+ *   q_weight, k_weight   device bf16 [D] or [heads][D], 8-byte aligned; NULL: ones.
+ *   num_k_heads    0: queries only, k arguments unused.
+ *   head_dim       64 or 128.
+ *   positions      device int32 [tokens][num_axes] (unused without a rotation).
+ * A token with a position outside the table is not written and recorded as WF_ERR_POSITION.
+ * tokens = 0 is a no-op.
+ */
+int wf_qk_norm_rope(const void* q, int64_t q_stride, void* q_out, const void* q_weight,
+                    int num_q_heads, const void* k, int64_t k_stride, void* k_out,
+                    const void* k_weight, int num_k_heads, int tokens, int head_dim,
+                    const int32_t* positions, const wf_norm_rope_t* rule, wf_stream_t stream);
+
+/*
+ * wf_kv_append_rope -- wf_kv_append of the consecutive chunks [chunk_begin, chunk_end) with the
+ * keys normed and rotated on the way; values are copied bit for bit.  k, v: the chunks' rows in
+ * order, [L][H][D] with k_stride / v_stride values from token to token, as q in wf_qk_norm_rope.
+ * k_weight, rule, positions ([L][num_axes], for the chunks' tokens) as there.  A token whose page
+ * is outside the pool or whose position is outside the table is not written (WF_ERR_PAGE_OOB,
+ * WF_ERR_POSITION).  Other errors as wf_kv_append; WF_ERR_INVALID_ARG for a bad chunk range.
+ */
+int wf_kv_append_rope(const wf_kv_pool_t* pool, int layer, int chunk_begin, int chunk_end,
+                      const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                      const void* k_weight, const int32_t* positions, const wf_norm_rope_t* rule,
+                      const int32_t* page_table, const wf_wavefront_t* wf, wf_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * FP8 cache: K/V held as e4m3 codes with one scale per block of 16 tokens and head, read in place
+ * by attention (the FP8 pool above is a transport format, converted back before attention).
+ * Half the memory and half the bytes a query token has to read.  Scales are powers of two, e8m0
+ * bytes b for 2^(b - 127), K and V apart:  value = e4m3(code) * 2^(b - 127).  A block's scale is
+ * the smallest power of two that brings its largest finite magnitude to 448 or less, its exponent
+ * kept in [-100, 119]; a value that is not finite is stored as NaN.
+ */
+typedef struct {
+  void* k_codes;       /* device e4m3 [num_pages][page_size][num_heads][head_dim], 16-byte aligned */
+  void* v_codes;
+  void* k_scale;       /* device e8m0 [num_pages][page_size / 16][num_heads] */
+  void* v_scale;
+  int32_t num_pages;
+  int32_t page_size;   /* tokens per page: a positive multiple of 16 */
+  int32_t num_heads;   /* key/value heads */
+  int32_t head_dim;    /* 64 or 128 */
+} wf_kv_pool_fp8_block_t;
+
+/*
+ * wf_kv_append_fp8_block -- append the chunks [chunk_begin, chunk_end) to an FP8 cache, keys normed
+ * and rotated on the way as by wf_kv_append_rope (rule NULL: neither), coded straight from fp32.
+ * Where the range starts or ends inside a block of 16 tokens, the block's other live rows -- those
+ * of logical tokens below chunk_offsets[num_chunks] -- stay: they are decoded, take part in the
+ * block's new scale and are coded again (exactly, but for values below 2^-6 of the new scale).
+ * Rows past the last token are left as they were, and so is everything outside the blocks that the
+ * range touches.  A pool must start out zeroed (all bytes 0), so that rows which no append has
+ * written yet stand for 0.  A block whose page is outside the pool, or with a new token whose
+ * position is outside the table, is not written (WF_ERR_PAGE_OOB, WF_ERR_POSITION).
+ * Arguments and other errors as wf_kv_append_rope.  Calls that touch the same block must be
+ * ordered (one stream).
+ */
+int wf_kv_append_fp8_block(const wf_kv_pool_fp8_block_t* pool, int layer, int chunk_begin,
+                           int chunk_end, const void* k, int64_t k_stride, const void* v,
+                           int64_t v_stride, const void* k_weight, const int32_t* positions,
+                           const wf_norm_rope_t* rule, const int32_t* page_table,
+                           const wf_wavefront_t* wf, wf_stream_t stream);
 
 /*
  * Rolling context window: the plan of one round of a stream (host only, no device work).
