@@ -38,6 +38,7 @@ _ABI_NAMES = (
     "attn_forward_i8", "QkI8", "Segments", "attn_forward_segments",
     "attn_segments_workspace_size", "WF_ERR_POSITION", "NormRope", "qk_norm_rope",
     "kv_append_rope", "kv_append_fp8_block", "KvPoolFp8Block",
+    "attn_forward_fp8_block", "attn_fp8_block_workspace_size",
 )
 __all__ = list(_ABI_NAMES)
 

@@ -36,7 +36,8 @@ EXPORTED = ("wf_kv_append", "wf_attn_forward", "wf_check_status", "wf_strerror",
             "wf_qk_i8_sizes", "wf_qk_quantize_i8", "wf_attn_forward_i8",
             "wf_attn_forward_segments", "wf_attn_segments_workspace_size",
             "wf_window_slots", "wf_window_round", "wf_window_round_ring", "wf_qk_norm_rope",
-            "wf_kv_append_rope", "wf_kv_append_fp8_block")
+            "wf_kv_append_rope", "wf_kv_append_fp8_block", "wf_attn_forward_fp8_block",
+            "wf_attn_fp8_block_workspace_size")
 
 
 class WfError(RuntimeError):
@@ -260,6 +261,12 @@ def _load(path: str = LIB_PATH) -> ctypes.CDLL:
                                            vp, i64, vp, vp, ctypes.POINTER(NormRopeC), vp,
                                            ctypes.POINTER(Wavefront), vp]
     lib.wf_kv_append_fp8_block.restype = i32
+    lib.wf_attn_forward_fp8_block.argtypes = [vp, i32, ctypes.POINTER(KvPoolFp8Block), vp,
+                                              ctypes.POINTER(SegmentsC), f32, vp, vp, i32, vp,
+                                              ctypes.c_size_t, vp]
+    lib.wf_attn_forward_fp8_block.restype = i32
+    lib.wf_attn_fp8_block_workspace_size.argtypes = [ctypes.POINTER(SegmentsC), i32, i32, i32, i32]
+    lib.wf_attn_fp8_block_workspace_size.restype = ctypes.c_size_t
     return lib
 
 
@@ -1144,6 +1151,51 @@ def kv_append_fp8_block(k_codes, v_codes, k_scale, v_scale, layer: int, chunk_be
                                     _stream_handle(stream))
     if rc != WF_OK:
         raise WfError(rc, "wf_kv_append_fp8_block")
+
+
+def attn_fp8_block_workspace_size(seg: Segments, num_q_heads: int, num_kv_heads: int,
+                                  head_dim: int, splits: int = 0) -> int:
+    """wf_attn_fp8_block_workspace_size: bytes of workspace attn_forward_fp8_block needs (0: none)."""
+    return int(lib.wf_attn_fp8_block_workspace_size(ctypes.byref(seg.c), int(num_q_heads),
+                                                    int(num_kv_heads), int(head_dim),
+                                                    int(splits)))
+
+
+def attn_forward_fp8_block(q, k_codes, v_codes, k_scale, v_scale, page_table_row, seg: Segments,
+                           scale: float, out, lse=None, splits: int = 0, workspace=None,
+                           stream=None) -> None:
+    """wf_attn_forward_fp8_block: rows of segment i of ``q`` ([T, Hq, D] bf16) see logical keys
+    [0, kv_end[i]) of an FP8 cache (see :func:`kv_append_fp8_block`) whose H heads each serve
+    Hq / H query heads; ``lse``: fp32 [Hq, T]."""
+    pool = _fp8_block_pool(k_codes, v_codes, k_scale, v_scale)
+    t_q = seg.t_q
+    if q.dim() != 3 or int(q.shape[0]) != t_q or int(q.shape[2]) != pool.head_dim or \
+            int(q.shape[1]) % pool.num_heads or q.shape[1] == 0:
+        raise ValueError(f"q: expected [{t_q}, a multiple of {pool.num_heads}, {pool.head_dim}], "
+                         f"got {tuple(q.shape)}")
+    if tuple(out.shape) != tuple(q.shape):
+        raise ValueError(f"out: expected {tuple(q.shape)}, got {tuple(out.shape)}")
+    Hq = int(q.shape[1])
+    _check_tensor(q, "q", "bf16")
+    _check_tensor(out, "out", "bf16")
+    _check_tensor(page_table_row, "page_table_row", "i32")
+    if page_table_row.dim() != 1 or page_table_row.numel() < seg.c.max_pages_per_seq:
+        raise ValueError(f"page_table_row: needs {seg.c.max_pages_per_seq} entries")
+    if lse is not None:
+        if tuple(lse.shape) != (Hq, t_q):
+            raise ValueError(f"lse: expected [{Hq}, {t_q}], got {tuple(lse.shape)}")
+        _check_tensor(lse, "lse", "f32")
+    if workspace is not None:
+        _check_tensor(workspace, "workspace", "u8")
+    _check_one_device(stream, q, out, k_codes, v_codes, k_scale, v_scale, page_table_row, lse,
+                      workspace)
+    rc = lib.wf_attn_forward_fp8_block(
+        q.data_ptr(), Hq, ctypes.byref(pool), page_table_row.data_ptr(), ctypes.byref(seg.c),
+        float(scale), out.data_ptr(), lse.data_ptr() if lse is not None else None, int(splits),
+        workspace.data_ptr() if workspace is not None else None,
+        workspace.numel() if workspace is not None else 0, _stream_handle(stream))
+    if rc != WF_OK:
+        raise WfError(rc, "wf_attn_forward_fp8_block")
 
 
 def ipc_export(device_ptr: int):

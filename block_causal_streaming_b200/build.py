@@ -22,7 +22,7 @@ SOURCES = [os.path.join(CSRC, "wf_api.cu"), os.path.join(CSRC, "wf_window.cpp")]
 DEPENDS = SOURCES + [os.path.join(CSRC, f) for f in ("sm100.cuh", "attn_kernel.cuh",
                                                       "append_kernel.cuh", "combine_kernel.cuh",
                                                       "fp8_kernel.cuh", "norm_rope_kernel.cuh",
-                                                      "fp8_block_kernel.cuh",
+                                                      "fp8_block_kernel.cuh", "attn_fp8_few_kernel.cuh",
                                                       "publish_kernel.cuh")] + \
     [os.path.join(ROOT, "include", "wf.h")]
 

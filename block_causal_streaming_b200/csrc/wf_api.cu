@@ -15,6 +15,7 @@
 
 #include "../../include/wf.h"
 #include "append_kernel.cuh"
+#include "attn_fp8_few_kernel.cuh"
 #include "attn_kernel.cuh"
 #include "combine_kernel.cuh"
 #include "fp8_block_kernel.cuh"
@@ -1598,6 +1599,187 @@ int wf_kv_append_fp8_block(const wf_kv_pool_fp8_block_t* pool, int layer, int ch
     else WF_LAUNCH(64, wfk::kRopeSplitPartial);
   }
 #undef WF_LAUNCH
+  return cudaGetLastError() == cudaSuccess ? WF_OK : WF_ERR_CUDA;
+}
+
+}  // extern "C"
+
+// -------------------------------------------------------- attention over the FP8 block cache
+namespace {
+
+constexpr int kMaxFp8Splits = 256;
+
+// The non-empty segments of a call: rows [row_end[i-1], row_end[i]) see keys [0, kv[i]).
+struct SegmentList {
+  int n = 0, t_q = 0, max_kv = 0;
+  int row_end[WF_MAX_CHUNKS], kv[WF_MAX_CHUNKS];
+  int rows(int i) const { return row_end[i] - (i > 0 ? row_end[i - 1] : 0); }
+};
+
+int segment_list(const wf_segments_t* seg, SegmentList* out) {
+  if (seg == nullptr || seg->rows_end == nullptr || seg->kv_end == nullptr)
+    return WF_ERR_INVALID_ARG;
+  if (seg->num_segments < 1 || seg->num_segments > WF_MAX_CHUNKS || seg->num_keys < 0)
+    return WF_ERR_SHAPE;
+  int prev = 0;
+  for (int i = 0; i < seg->num_segments; ++i) {
+    if (seg->rows_end[i] < prev || seg->kv_end[i] < 0 || seg->kv_end[i] > seg->num_keys)
+      return WF_ERR_SHAPE;
+    if (seg->rows_end[i] == prev) continue;
+    prev = seg->rows_end[i];
+    out->row_end[out->n] = prev;
+    out->kv[out->n] = seg->kv_end[i];
+    out->max_kv = std::max(out->max_kv, seg->kv_end[i]);
+    ++out->n;
+  }
+  out->t_q = prev;
+  return WF_OK;
+}
+
+// What a call launches: tiles of 16 mt packed rows, each segment on its own, and key parts.
+struct Fp8Plan {
+  int mt = 1, tiles = 0, splits = 1;
+  int tile_end[WF_MAX_CHUNKS];
+};
+
+int fp8_plan(const SegmentList& sl, int Hq, int Hk, int splits, int num_sms, Fp8Plan* plan) {
+  const int64_t group = Hq / Hk;
+  int64_t most = 0, tiles = 0;
+  for (int i = 0; i < sl.n; ++i) most = std::max(most, sl.rows(i) * group);
+  plan->mt = most > 16 ? 2 : 1;
+  for (int i = 0; i < sl.n; ++i) {
+    tiles += (sl.rows(i) * group + 16 * plan->mt - 1) / (16 * plan->mt);
+    plan->tile_end[i] = static_cast<int>(std::min<int64_t>(tiles, INT32_MAX));
+  }
+  if (tiles * Hk * kMaxFp8Splits > INT32_MAX) return WF_ERR_SHAPE;
+  plan->tiles = static_cast<int>(tiles);
+  const int blocks = (sl.max_kv + 15) / 16;
+  if (splits == 0) {
+    // enough parts to fill the SMs, but two blocks of keys at least for every warp
+    const int64_t want = static_cast<int64_t>(num_sms) * (plan->mt == 1 ? 2 : 1);
+    splits = static_cast<int>(std::max<int64_t>(1, want / (tiles * Hk)));
+    splits = std::min(splits, blocks / (2 * wfk::kFewWarps));
+  }
+  plan->splits = std::max(1, std::min({splits, kMaxFp8Splits, blocks}));
+  return WF_OK;
+}
+
+size_t fp8_workspace_bytes(const SegmentList& sl, const Fp8Plan& plan, int Hq, int D) {
+  if (plan.splits <= 1) return 0;
+  const size_t rows = static_cast<size_t>(plan.splits) * sl.t_q * Hq;
+  return align256(rows * D * sizeof(float)) + align256(rows * sizeof(float));
+}
+
+template <int D, int MT>
+int launch_few(const wfk::AttnFewParams& p, cudaStream_t s) {
+  auto kernel = wfk::wf_attn_fp8_few_kernel<D, MT>;
+  const int bytes = static_cast<int>(wfk::FewSmem<D, MT>::BYTES);
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
+      cudaSuccess) {
+    cudaGetLastError();
+    return WF_ERR_CUDA;
+  }
+  const unsigned grid = static_cast<unsigned>(p.tiles) * p.Hk * p.splits;
+  kernel<<<grid, wfk::kFewThreads, bytes, s>>>(p);
+  return cudaGetLastError() == cudaSuccess ? WF_OK : WF_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t wf_attn_fp8_block_workspace_size(const wf_segments_t* segments, int num_q_heads,
+                                        int num_kv_heads, int head_dim, int splits) {
+  SegmentList sl;
+  if (num_q_heads < 1 || num_kv_heads < 1 || num_q_heads % num_kv_heads != 0 || splits < 0 ||
+      (head_dim != 64 && head_dim != 128) || segment_list(segments, &sl) != WF_OK || sl.t_q == 0)
+    return 0;
+  int sms = 0;
+  if (splits == 0) {
+    DeviceState* d = nullptr;
+    if (device_state(&d) != WF_OK) return 0;
+    sms = d->num_sms;
+  }
+  Fp8Plan plan;
+  if (fp8_plan(sl, num_q_heads, num_kv_heads, splits, sms, &plan) != WF_OK) return 0;
+  return fp8_workspace_bytes(sl, plan, num_q_heads, head_dim);
+}
+
+int wf_attn_forward_fp8_block(const void* q, int num_q_heads,
+                              const wf_kv_pool_fp8_block_t* kv_pages,
+                              const int32_t* page_table_row, const wf_segments_t* segments,
+                              float scale, void* out, float* lse_or_null, int splits,
+                              void* workspace, size_t workspace_bytes, wf_stream_t stream) {
+  int rc = validate_pool_fp8_block(kv_pages);
+  if (rc) return rc;
+  SegmentList sl;
+  rc = segment_list(segments, &sl);
+  if (rc) return rc;
+  const int Hk = kv_pages->num_heads, D = kv_pages->head_dim, ps = kv_pages->page_size;
+  if (num_q_heads < 1 || num_q_heads % Hk != 0) return WF_ERR_SHAPE;
+  const int64_t pages = (static_cast<int64_t>(segments->num_keys) + ps - 1) / ps;
+  if (segments->max_pages_per_seq < 0 || pages > segments->max_pages_per_seq)
+    return WF_ERR_CAPACITY;
+  if (!(scale > 0.f) || !std::isfinite(scale) || splits < 0) return WF_ERR_INVALID_ARG;
+  if (sl.t_q == 0) return WF_OK;
+  if (q == nullptr || out == nullptr || page_table_row == nullptr || !aligned16(q) ||
+      !aligned16(out) || (reinterpret_cast<uintptr_t>(page_table_row) & 3u) ||
+      (reinterpret_cast<uintptr_t>(lse_or_null) & 3u))
+    return WF_ERR_INVALID_ARG;
+  DeviceState* d = nullptr;
+  rc = device_state(&d);
+  if (rc) return rc;
+  Fp8Plan plan;
+  rc = fp8_plan(sl, num_q_heads, Hk, splits, d->num_sms, &plan);
+  if (rc) return rc;
+  wfk::AttnFewParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.k_codes = static_cast<const uint8_t*>(kv_pages->k_codes);
+  p.v_codes = static_cast<const uint8_t*>(kv_pages->v_codes);
+  p.k_scale = static_cast<const uint8_t*>(kv_pages->k_scale);
+  p.v_scale = static_cast<const uint8_t*>(kv_pages->v_scale);
+  p.page_table = page_table_row;
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.lse = lse_or_null;
+  p.status = d->status;
+  p.T_q = sl.t_q;
+  p.Hq = num_q_heads;
+  p.Hk = Hk;
+  p.group = num_q_heads / Hk;
+  p.page_size = ps;
+  p.num_pages = kv_pages->num_pages;
+  p.splits = plan.splits;
+  p.tiles = plan.tiles;
+  p.sl2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+  p.nseg = sl.n;
+  for (int i = 0; i < sl.n; ++i) {
+    p.seg_tile_end[i] = plan.tile_end[i];
+    p.seg_row_end[i] = sl.row_end[i];
+    p.seg_kv[i] = sl.kv[i];
+  }
+  if (plan.splits > 1) {
+    if (workspace == nullptr || !aligned16(workspace)) return WF_ERR_INVALID_ARG;
+    if (workspace_bytes < fp8_workspace_bytes(sl, plan, num_q_heads, D)) return WF_ERR_CAPACITY;
+    const size_t rows = static_cast<size_t>(plan.splits) * sl.t_q * num_q_heads;
+    p.part_o = static_cast<float*>(workspace);
+    p.part_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) +
+                                          align256(rows * D * sizeof(float)));
+  }
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (D == 128) rc = plan.mt == 1 ? launch_few<128, 1>(p, s) : launch_few<128, 2>(p, s);
+  else rc = plan.mt == 1 ? launch_few<64, 1>(p, s) : launch_few<64, 2>(p, s);
+  if (rc || plan.splits == 1) return rc;
+  const int64_t threads = static_cast<int64_t>(sl.t_q) * num_q_heads * 32;
+  const unsigned blocks =
+      static_cast<unsigned>((threads + wfk::kCombineThreads - 1) / wfk::kCombineThreads);
+  const wfk::CombinePlan cp{plan.splits, 0, 1, num_q_heads, sl.t_q};
+  if (D == 128)
+    wfk::wf_combine_kernel<128><<<blocks, wfk::kCombineThreads, 0, s>>>(
+        p.part_o, p.part_lse, cp, sl.t_q, num_q_heads, p.out, p.lse);
+  else
+    wfk::wf_combine_kernel<64><<<blocks, wfk::kCombineThreads, 0, s>>>(
+        p.part_o, p.part_lse, cp, sl.t_q, num_q_heads, p.out, p.lse);
   return cudaGetLastError() == cudaSuccess ? WF_OK : WF_ERR_CUDA;
 }
 

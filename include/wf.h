@@ -567,6 +567,38 @@ int wf_kv_append_fp8_block(const wf_kv_pool_fp8_block_t* pool, int layer, int ch
                            const wf_wavefront_t* wf, wf_stream_t stream);
 
 /*
+ * wf_attn_forward_fp8_block -- attention of query segments straight over an FP8 cache: the codes are
+ * what is read, no bf16 copy of the keys or values is made.
+ *   q               device bf16 [rows_end[last]][num_q_heads][D], 16-byte aligned, contiguous.
+ *   num_q_heads     a multiple of kv_pages->num_heads: query head h reads K/V head
+ *                   h / (num_q_heads / num_heads).
+ *   kv_pages        the FP8 cache; every key below the largest kv_end must have been appended.  Rows
+ *                   past it may hold anything, NaN included.
+ *   segments        as in wf_attn_forward_segments, except that a limit may also be 0 (the rows see
+ *                   no key: out 0, lse -inf) and limits may come in any order.
+ *   out             device bf16, laid out as q: softmax(scale q K^T) V over the rows' keys, on the
+ *                   values the cache stands for.  fp32 statistics and accumulation; weights are
+ *                   rounded to 11 bits or more before P.V.
+ *   lse_or_null     device fp32 [num_q_heads][rows] (optional).
+ *   splits          S >= 1: every row's keys in S parts (at most 256), joined by a second launch; 0:
+ *                   the library chooses.
+ *   workspace       device memory, 16-byte aligned, wf_attn_fp8_block_workspace_size bytes for the
+ *                   same arguments; may be null when that is 0.  Not shared by calls, or captured
+ *                   graphs, that may run at the same time.
+ * A page outside the pool is read as page 0 and recorded (WF_ERR_PAGE_OOB).  Errors:
+ * WF_ERR_INVALID_ARG for null or misaligned pointers, scale <= 0, splits < 0; WF_ERR_SHAPE for
+ * segments or head counts that break the rules; WF_ERR_CAPACITY when num_keys needs more than
+ * max_pages_per_seq pages or the workspace is too small.  No rows: a no-op.
+ */
+int wf_attn_forward_fp8_block(const void* q, int num_q_heads,
+                              const wf_kv_pool_fp8_block_t* kv_pages,
+                              const int32_t* page_table_row, const wf_segments_t* segments,
+                              float scale, void* out, float* lse_or_null, int splits,
+                              void* workspace, size_t workspace_bytes, wf_stream_t stream);
+size_t wf_attn_fp8_block_workspace_size(const wf_segments_t* segments, int num_q_heads,
+                                        int num_kv_heads, int head_dim, int splits);
+
+/*
  * Rolling context window: the plan of one round of a stream (host only, no device work).
  *
  * The pages' rules:
