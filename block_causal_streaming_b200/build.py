@@ -23,6 +23,7 @@ DEPENDS = SOURCES + [os.path.join(CSRC, f) for f in ("sm100.cuh", "attn_kernel.c
                                                       "append_kernel.cuh", "combine_kernel.cuh",
                                                       "fp8_kernel.cuh", "norm_rope_kernel.cuh",
                                                       "fp8_block_kernel.cuh", "attn_fp8_few_kernel.cuh",
+                                                      "attn_fp8_kernel.cuh",
                                                       "publish_kernel.cuh")] + \
     [os.path.join(ROOT, "include", "wf.h")]
 
@@ -46,29 +47,32 @@ def needs_build(lib: str = LIB) -> bool:
     return any(os.path.getmtime(f) > t for f in DEPENDS if os.path.exists(f))
 
 
-# The attention kernel splits its register file with setmaxnreg assuming it is launched with
-# 168 registers per thread (384 threads); a different count would make the split wait forever.
-ATTN_LAUNCH_REGS = 168
+# The attention kernels split their register file with setmaxnreg assuming a launch with 168
+# registers per thread (384 threads; 128 and 512 threads for the FP8 cache's); a different count
+# would make the split wait forever.
+ATTN_LAUNCH_REGS = {"wf_attn_fwd_kernel": 168, "wf_attn_fp8_kernel": 128}
 
 
 def check_register_counts(ptxas_log: str) -> None:
-    """Fail the build unless every attention kernel was compiled for ATTN_LAUNCH_REGS."""
+    """Fail the build unless every attention kernel was compiled for its ATTN_LAUNCH_REGS."""
     entry = None
-    found = 0
+    found = set()
     for line in ptxas_log.splitlines():
         m = re.search(r"Compiling entry function '([^']+)'", line)
         if m:
             entry = m.group(1)
             continue
         m = re.search(r"Used (\d+) registers", line)
-        if m and entry and "wf_attn_fwd_kernel" in entry:
-            found += 1
-            if int(m.group(1)) != ATTN_LAUNCH_REGS:
-                raise RuntimeError(f"{entry}: {m.group(1)} registers, expected {ATTN_LAUNCH_REGS}"
-                                   " (the setmaxnreg split in attn_kernel.cuh depends on it)")
+        kernel = next((k for k in ATTN_LAUNCH_REGS if entry and k in entry), None)
+        if m and kernel:
+            found.add(kernel)
+            if int(m.group(1)) != ATTN_LAUNCH_REGS[kernel]:
+                raise RuntimeError(f"{entry}: {m.group(1)} registers, expected "
+                                   f"{ATTN_LAUNCH_REGS[kernel]} (the kernel's setmaxnreg split "
+                                   "depends on it)")
             entry = None
-    if found == 0:
-        raise RuntimeError("ptxas reported no attention kernel")
+    if found != set(ATTN_LAUNCH_REGS):
+        raise RuntimeError("ptxas did not report every attention kernel")
 
 
 def build(verbose: bool = False, force: bool = False, out: str = LIB) -> str:

@@ -1,0 +1,618 @@
+// attn_fp8_kernel.cuh -- attention straight over the FP8 cache for many query rows (sm_100a,
+// tcgen05 + TMEM + TMA).
+//
+// The block-causal attention kernel's design (two 128-row Q tiles per CTA share every K/V tile,
+// one S buffer the tiles take turns in, P in its own TMEM columns, QK^T and P.V issued by two
+// threads) on keys and values that arrive as e4m3 codes, 16 KB a tile instead of 32:
+//   - QK^T runs on the codes as they are (kind::f8f6f4).  A bf16 query value has 8 significant bits
+//     and e4m3 has 4, so each row is split once into two e4m3 rows, hi + lo, under a power of two
+//     for the row; S = hi K^T + lo K^T is the exact product for values down to 2^-10 of the row's
+//     largest (and within 2^-18 of that largest below), at the time of one bf16 product.  Four
+//     threads' worth of conversion per key and tile would be the other way (K to bf16).
+//   - The key scale of each 16 keys multiplies its 16 columns of S, inside the multiply-add that
+//     subtracts the maximum; the maximum is taken over the 8 blocks' scaled maxima.
+//   - Values go to f16 (exact) in shared memory, by four converter warps: 16 codes a step, times
+//     2^(e_v - E + 7), E the largest value exponent of this CTA's keys (read up front; one byte for
+//     16 keys).  What a block with a small scale loses lies below 2^-40 of the largest value.
+//     f16 rather than bf16: one instruction widens two codes, and the weights keep 11 bits.
+//   - Weights are f16, p 2^13 against a reference that trails the maximum by at most 2^2, so
+//     p 2^13 <= 2^15: 11 bits down to 2^-27 of the largest weight, then steps of 2^-37 of it.
+//     The row sum adds the weights before rounding, two at a time (so lse is good to fp32; a sum
+//     of the rounded ones is off by 2^-12 / sqrt(keys)).  (A reference that may trail by 2^8, as where weights
+//     are bf16, would leave f16 no room: steps of 2^-31, seen where blocks' values differ by 2^20.)
+//
+// A unit is one K/V head and up to 256 packed rows of ONE query segment; packed row m is query row
+// m / group, head m % group of the K/V head's group, so heads that share keys share the tiles too.
+// With one limit per unit nothing a row may not see is ever multiplied with a weight of 0 (0 x NaN):
+// tiles past the limit are not read, the last tile's columns past it get weight 0 and its values
+// are zeroed.
+//
+// Warp roles (512 threads): 0-3, 4-7 softmax of Q tile 0, 1 (thread = row; they also split Q);
+// 8 TMA of K, key scales; 9 issues QK^T; 10 issues P.V; 11 TMA of V codes; 12-15 convert V.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+
+#include <cfloat>
+
+#include "attn_fp8_few_kernel.cuh"
+#include "attn_kernel.cuh"
+#include "fp8_block_kernel.cuh"
+
+namespace wfk {
+
+constexpr int kFp8AttnThreads = 512;
+constexpr int kFp8LaunchRegs = 128;          // 65536 / 512
+constexpr int kFp8RegSoftmax = 200, kFp8RegOther = 2 * kFp8LaunchRegs - kFp8RegSoftmax;
+static_assert(kFp8RegSoftmax % 8 == 0 && kFp8RegOther % 8 == 0 && kFp8RegOther >= 24,
+              "setmaxnreg counts are multiples of 8");
+static_assert(256 * kFp8RegSoftmax + 256 * kFp8RegOther <= 512 * kFp8LaunchRegs,
+              "split exceeds the launch");
+
+constexpr float kTrail = 2.f, kShift = 15.f - kTrail;   // weights: at most 2^15
+
+struct AttnFp8Params {
+  CUtensorMap tm_k;  // e4m3 (D, Hk, num_pages * page_size), box (D, 1, box_rows), D-byte swizzle
+  CUtensorMap tm_v;
+  const __nv_bfloat16* q;
+  const uint8_t* k_scale;
+  const uint8_t* v_scale;
+  const int* page_table;
+  __nv_bfloat16* out;
+  float* lse;
+  float* part_o;
+  float* part_lse;
+  int* status;
+  unsigned* grid_abort;
+  unsigned launch_id;
+  int T_q, Hq, Hk, group, page_size, num_pages, total_rows, box_rows, splits;
+  int head_group;                    // K/V heads per dispatch group (divides Hk)
+  int pairs;                         // row blocks of all segments
+  float sl2;                         // scale * log2(e)
+  // segments in dispatch order (most keys first)
+  int seg_pair_end[kFewSegs];        // row blocks up to and including segment i
+  int seg_row0[kFewSegs];
+  int seg_rows[kFewSegs];
+  int seg_kv[kFewSegs];
+};
+
+template <int D>
+struct AttnFp8Smem {
+  static constexpr int BN = kBN;
+  static constexpr int DH = D / 64;                       // 128-byte halves of an f16 value row
+  static constexpr int NK = D == 128 ? 4 : 6;             // K slots
+  static constexpr int NC = D == 128 ? 2 : 4;             // V code slots
+  static constexpr int NV = D == 128 ? 2 : 4;             // V f16 slots
+  static constexpr uint32_t QTERM = kBM * D;              // one e4m3 term of a Q tile
+  static constexpr uint32_t CTILE = BN * D;               // a tile of codes
+  static constexpr uint32_t VHALF = BN * 128u;
+  static constexpr uint32_t VTILE = DH * VHALF;           // a tile of f16 values
+  static constexpr uint32_t Q_OFF = 0;                    // [2 tiles][hi, lo]
+  static constexpr uint32_t K_OFF = Q_OFF + 4 * QTERM;
+  static constexpr uint32_t C_OFF = K_OFF + NK * CTILE;
+  static constexpr uint32_t V_OFF = C_OFF + NC * CTILE;
+  static constexpr uint32_t KS_OFF = V_OFF + NV * VTILE;  // key scales [2 NK][8] floats
+  static constexpr uint32_t BAR_OFF = KS_OFF + 2 * NK * 32;
+  static constexpr int B_Q = 0, B_KF = 1, B_KE = B_KF + NK, B_CF = B_KE + NK, B_CE = B_CF + NC,
+                       B_VF = B_CE + NC, B_VE = B_VF + NV, B_S = B_VE + NV, B_P = B_S + 2,
+                       B_O = B_P + 2, B_SF = B_O + 2, B_EM = B_SF + 1, B_DRAIN = B_EM + 1,
+                       NBAR = B_DRAIN + 2;
+  static constexpr uint32_t MISC_OFF = BAR_OFF + NBAR * 8;
+  static constexpr uint32_t BYTES = MISC_OFF + 32;
+  static constexpr uint32_t ALLOC = BYTES + 1024;         // slack for 1024-byte alignment
+  static_assert(ALLOC <= 227u * 1024u, "shared memory per CTA exceeds 227 KB");
+};
+
+// Offset of 16-byte piece c of row r in a tile of D-byte rows under the D-byte swizzle.
+template <int D>
+__device__ __forceinline__ uint32_t swz(int r, int c) {
+  return D == 128 ? static_cast<uint32_t>(r * 128 + ((c ^ (r & 7)) * 16))
+                  : static_cast<uint32_t>(r * 64 + ((c ^ ((r >> 1) & 3)) * 16));
+}
+
+// Shared-memory matrix descriptor of a K-major tile of D-byte rows under the D-byte swizzle.
+template <int D>
+__device__ __forceinline__ uint64_t smem_desc_codes(uint32_t start) {
+  if (D == 128) return smem_desc_sw128(start, 16, 1024);
+  uint64_t d = 0;                                         // 64-byte swizzle: 8 rows are 512 bytes
+  d |= static_cast<uint64_t>((start >> 4) & 0x3FFFu);
+  d |= static_cast<uint64_t>(1u) << 16;
+  d |= static_cast<uint64_t>(512u >> 4) << 32;
+  d |= static_cast<uint64_t>(1u) << 46;
+  d |= static_cast<uint64_t>(4u) << 61;
+  return d;
+}
+
+// Instruction descriptor for kind::f16 with f16 A/B, B MN-major, and fp32 accumulation.
+__host__ __device__ constexpr uint32_t idesc_f16_f32_bmn(int M, int N) {
+  return (1u << 4) | (1u << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
+         (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+__device__ __forceinline__ void st_shared_v4(uint32_t a, uint32_t x, uint32_t y, uint32_t z,
+                                             uint32_t w) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w)
+               : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 ld_shared_f4(uint32_t a) {
+  const uint4 v = ld_shared_v4(a);
+  return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z),
+                     __uint_as_float(v.w));
+}
+
+// Pool row of logical token `tok`; a page outside the pool is recorded and read as page 0.
+__device__ __forceinline__ int fp8_row(const AttnFp8Params& p, int tok) {
+  const int idx = tok / p.page_size;
+  int pg = __ldg(p.page_table + idx);
+  if (pg < 0 || pg >= p.num_pages) {
+    atomicCAS(p.status, 0, 5 /* WF_ERR_PAGE_OOB */);
+    pg = 0;
+  }
+  return pg * p.page_size + (tok - idx * p.page_size);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kFp8AttnThreads, 1)
+    wf_attn_fp8_kernel(const __grid_constant__ AttnFp8Params p) {
+  using L = AttnFp8Smem<D>;
+  constexpr int BN = L::BN, NK = L::NK, NC = L::NC, NV = L::NV;
+
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* const base_ptr = smem_raw + (base - raw);
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(base_ptr + L::MISC_OFF);
+  volatile int* const cta_abort = reinterpret_cast<volatile int*>(base_ptr + L::MISC_OFF + 4);
+  int* const emax_slot = reinterpret_cast<int*>(base_ptr + L::MISC_OFF + 8);
+  auto bar = [&](int i) -> uint32_t { return base + L::BAR_OFF + 8u * static_cast<uint32_t>(i); };
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // unit and part of this CTA: parts of a unit are neighbours; K/V heads go in groups, every row
+  // block of a group, longest first, heads fastest, before the next group
+  const int unit = static_cast<int>(blockIdx.x) / p.splits;
+  const int split = static_cast<int>(blockIdx.x) - unit * p.splits;
+  const int per_group = p.pairs * p.head_group;
+  const int hgrp = unit / per_group, in_group = unit - hgrp * per_group;
+  const int pair_all = in_group / p.head_group;
+  const int head = hgrp * p.head_group + in_group % p.head_group;
+  int seg = 0;
+  while (pair_all >= p.seg_pair_end[seg]) ++seg;
+  const int m0 = (pair_all - (seg > 0 ? p.seg_pair_end[seg - 1] : 0)) * (2 * kBM);
+  const int m_total = p.seg_rows[seg] * p.group;        // packed rows of the segment
+  const int nq = m0 + kBM < m_total ? 2 : 1;            // Q tiles with rows
+  const int n_max = p.seg_kv[seg];
+  const int n_tiles = (n_max + BN - 1) / BN;
+  const int kb = static_cast<int>(static_cast<int64_t>(split) * n_tiles / p.splits);
+  const int nk = static_cast<int>(static_cast<int64_t>(split + 1) * n_tiles / p.splits) - kb;
+
+  const WaitCtx w{cta_abort, p.grid_abort, p.status, p.launch_id, 6 /* WF_ERR_TIMEOUT */,
+                  kWaitTimeoutNs};
+  if (threadIdx.x == 0) {
+    *cta_abort = (*reinterpret_cast<volatile unsigned*>(p.grid_abort) == p.launch_id) ? 1 : 0;
+    for (int i = 0; i < L::NBAR; ++i) {
+      uint32_t count = 1;
+      if (i == L::B_Q) count = 128u * nq;
+      else if (i >= L::B_CE && i < L::B_VE) count = 128u;       // V codes read, V f16 written
+      else if (i >= L::B_S && i < L::B_P) count = 2u;           // commit and the issuer itself
+      else if (i >= L::B_P && i < L::B_O) count = 128u;
+      else if (i == L::B_SF) count = 4u;
+      mbar_init(bar(i), count);
+    }
+    mbar_init_fence();
+  }
+  if (warp == 8) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const bool skip = *cta_abort != 0;
+
+  if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kFp8RegSoftmax) : "memory");
+    const int q = warp >> 2, wq = warp & 3;
+    if (!skip && q < nq) {
+      // ------------------------------------------------------------------ softmax warpgroups
+      const int row = wq * 32 + lane;                       // row within the Q tile == TMEM lane
+      const int m = m0 + q * kBM + row;                     // packed row
+      const bool live = m < m_total;
+      const int64_t qrow = p.seg_row0[seg] + m / p.group;
+      const int qhead = head * p.group + m % p.group;
+      const int64_t orow = qrow * p.Hq + qhead;
+      float sl2;
+      {
+        // split this row into hi + lo e4m3 under 2^-e, and store both K-major
+        uint4 x[D / 8];
+        const uint4* src = reinterpret_cast<const uint4*>(p.q + orow * D);
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) x[c] = live ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+        uint32_t mw = 0;                                    // largest |x|, as a bit pattern
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          mw = __vmaxu2(mw, x[c].x & 0x7FFF7FFFu);
+          mw = __vmaxu2(mw, x[c].y & 0x7FFF7FFFu);
+          mw = __vmaxu2(mw, x[c].z & 0x7FFF7FFFu);
+          mw = __vmaxu2(mw, x[c].w & 0x7FFF7FFFu);
+        }
+        const int e = scale_exponent(__uint_as_float(max(mw & 0xFFFFu, mw >> 16) << 16));
+        const float f = exp2_int(-e);
+        sl2 = p.sl2 * exp2_int(e);
+        const uint32_t hi_t = base + L::Q_OFF + 2 * q * L::QTERM, lo_t = hi_t + L::QTERM;
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {
+          uint32_t hw[4], lw[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {                     // 4 values: two words of bf16
+            const uint4 v = x[2 * c + (i >> 1)];
+            const uint32_t w0 = (i & 1) ? v.z : v.x, w1 = (i & 1) ? v.w : v.y;
+            float y[4];
+            unpack4(make_uint2(w0, w1), y);
+            float back[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) y[k] *= f;
+            hw[i] = encode4(y);
+            decode4(hw[i], 1.f, back);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) y[k] -= back[k];
+            lw[i] = encode4(y);
+          }
+          st_shared_v4(hi_t + swz<D>(row, c), hw[0], hw[1], hw[2], hw[3]);
+          st_shared_v4(lo_t + swz<D>(row, c), lw[0], lw[1], lw[2], lw[3]);
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(bar(L::B_Q));
+      }
+      const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
+      const uint32_t tS = tmem + lane_off;                               // the shared S buffer
+      const uint32_t tP = tmem + lane_off + 128u + static_cast<uint32_t>(q * 64);
+      const uint32_t tO = tmem + lane_off + 256u + static_cast<uint32_t>(q * D);
+      float m2 = -INFINITY;   // running reference of the base-2 logits
+      float l = 0.f;          // running sum of exp2(t - m2 + kShift)
+      bool ok = true;
+      for (int j = 0; j < nk; ++j) {
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(L::B_S + q), j & 1, w));
+        if (!ok) break;
+        tc_fence_after();
+        float s[BN];
+        {
+          uint32_t r[BN];
+#pragma unroll
+          for (int c = 0; c < BN / 32; ++c)
+            tmem_ld32(tS + 32u * c, *reinterpret_cast<uint32_t(*)[32]>(&r[32 * c]));
+          tmem_wait_ld();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(L::B_SF));
+#pragma unroll
+          for (int c = 0; c < BN; ++c) s[c] = __uint_as_float(r[c]);
+        }
+        // logit factor of each block of 16 keys; kept positive so a masked column stays -inf
+        const uint32_t ks = base + L::KS_OFF + static_cast<uint32_t>(j % (2 * NK)) * 32u;
+        const float4 ka = ld_shared_f4(ks), kc = ld_shared_f4(ks + 16);
+        float f[8] = {ka.x, ka.y, ka.z, ka.w, kc.x, kc.y, kc.z, kc.w};
+#pragma unroll
+        for (int b = 0; b < 8; ++b) f[b] = fmaxf(f[b] * sl2, FLT_MIN);
+        const int lim = n_max - (kb + j) * BN;              // visible columns of this tile
+        if (lim < BN) {
+#pragma unroll
+          for (int c = 0; c < BN; ++c) s[c] = (c < lim) ? s[c] : -INFINITY;
+        }
+        float bm[8];
+#pragma unroll
+        for (int b = 0; b < 8; ++b) {
+          const float* t = s + 16 * b;
+          const float u = max3(t[0], t[1], t[2]), v = max3(t[3], t[4], t[5]);
+          const float x = max3(t[6], t[7], t[8]), y = max3(t[9], t[10], t[11]);
+          bm[b] = max3(max3(u, v, x), max3(y, t[12], t[13]), fmaxf(t[14], t[15])) * f[b];
+        }
+        const float tmax = max3(max3(bm[0], bm[1], bm[2]), max3(bm[3], bm[4], bm[5]),
+                                fmaxf(bm[6], bm[7]));
+        // the reference moves only when the maximum exceeds it by more than 2^kTrail
+        const bool need = tmax > m2 + kTrail;
+        float alpha = 1.f;
+        if (need) {
+          alpha = ex2_approx(m2 - tmax);                    // 0 on the first visible tile
+          m2 = tmax;
+        }
+        const float mref = m2 == -INFINITY ? 0.f : m2 - kShift;
+        const float2 negm = make_float2(-mref, -mref);
+        float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
+                         make_float2(0.f, 0.f)};
+        uint32_t pk[BN / 2];
+#pragma unroll
+        for (int i = 0; i < BN / 2; ++i) {
+          const float2 x = __ffma2_rn(make_float2(s[2 * i], s[2 * i + 1]),
+                                      make_float2(f[i / 8], f[i / 8]), negm);
+          const float2 e = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+          pk[i] = pack_f16x2(e.x, e.y);
+          acc[i & 3] = __fadd2_rn(acc[i & 3], e);
+        }
+        if (j > 0) {
+          ok = __all_sync(0xffffffffu, mbar_wait(bar(L::B_O + q), (j - 1) & 1, w));
+          if (!ok) break;
+          tc_fence_after();
+          if (__any_sync(0xffffffffu, need)) {
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t r[32];
+              tmem_ld32(tO + 32u * c, r);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha);
+              tmem_st32(tO + 32u * c, r);
+            }
+          }
+        }
+#pragma unroll
+        for (int h = 0; h < BN / 64; ++h)
+          tmem_st32(tP + 32u * h, *reinterpret_cast<uint32_t(*)[32]>(&pk[32 * h]));
+        {
+          const float2 t = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
+          l = l * alpha + (t.x + t.y);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(bar(L::B_P + q));
+      }
+      // ------------------------------------------------------------------------- epilogue
+      float inv = 0.f;
+      if (nk > 0) {
+        if (ok)
+          ok = __all_sync(0xffffffffu, mbar_wait(bar(L::B_O + q), (nk - 1) & 1, w) &&
+                                           mbar_wait(bar(L::B_EM), 0, w));
+        tc_fence_after();
+        if (ok) inv = l == 0.f ? 0.f : pow2f(*emax_slot - 7) / l;
+      }
+      if (ok) {
+        // O / l: bf16 into `out`, or fp32 into the partials of a split; 0 and -inf for rows that
+        // see no key (of the part)
+        const bool part = p.splits > 1;
+        const int64_t prow = static_cast<int64_t>(split) * p.T_q * p.Hq + orow;
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t r[32];
+          if (nk > 0) {
+            tmem_ld32(tO + 32u * c, r);
+            tmem_wait_ld();
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) r[i] = 0u;
+          }
+          if (live && part) {
+            float4* dst = reinterpret_cast<float4*>(p.part_o + prow * D + 32 * c);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              dst[i] = make_float4(
+                  __uint_as_float(r[4 * i]) * inv, __uint_as_float(r[4 * i + 1]) * inv,
+                  __uint_as_float(r[4 * i + 2]) * inv, __uint_as_float(r[4 * i + 3]) * inv);
+          } else if (live) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              pk[i] = pack_bf16x2(__uint_as_float(r[2 * i]) * inv,
+                                  __uint_as_float(r[2 * i + 1]) * inv);
+            uint4* dst = reinterpret_cast<uint4*>(p.out + orow * D + 32 * c);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              dst[i] = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+          }
+        }
+        const float lse = l == 0.f ? -INFINITY : (m2 - kShift + __log2f(l)) * 0.69314718056f;
+        if (live && part)
+          p.part_lse[(static_cast<int64_t>(split) * p.Hq + qhead) * p.T_q + qrow] = lse;
+        else if (live && p.lse != nullptr)
+          p.lse[static_cast<int64_t>(qhead) * p.T_q + qrow] = lse;
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFp8RegOther) : "memory");
+    if (skip || nk == 0) {
+      // nothing to load or multiply
+    } else if (warp == 8 || warp == 11) {
+      // ------------------------------------------------------------------------ TMA producers
+      const bool is_k = warp == 8;
+      const CUtensorMap* map = is_k ? &p.tm_k : &p.tm_v;
+      const int ns = is_k ? NK : NC;
+      const int bf = is_k ? L::B_KF : L::B_CF, be = is_k ? L::B_KE : L::B_CE;
+      const uint32_t dst0 = base + (is_k ? L::K_OFF : L::C_OFF);
+      const int R = p.box_rows, nb = BN / R;               // page boxes per tile (<= BN / 16)
+      if (lane == 0) tma_prefetch_desc(map);
+      auto box_row = [&](int t, int b) -> int {            // past the pool (zeros) beyond n_max
+        const int tok = (kb + t) * BN + b * R;
+        if (b >= nb || t >= nk || tok >= n_max) return p.total_rows;
+        return fp8_row(p, tok);
+      };
+      // key scale of block `lane` of a tile (lanes 0..7)
+      auto key_scale = [&](int t) -> float {
+        const int tok = (kb + t) * BN + lane * 16;
+        if (!is_k || lane >= 8 || t >= nk || tok >= n_max) return 1.f;
+        const int r = fp8_row(p, tok);
+        const uint32_t b = __ldg(p.k_scale + static_cast<int64_t>(r / 16) * p.Hk + head);
+        return __uint_as_float(b << 23);
+      };
+      bool ok = true;
+      int issued = 0;
+      int coord_next = box_row(0, lane);                   // looked up one tile ahead
+      float ks_next = key_scale(0);
+      for (int j = 0; j < nk && ok; ++j) {
+        const int coord = coord_next;
+        const float ks = ks_next;
+        if (j + 1 < nk) {
+          coord_next = box_row(j + 1, lane);
+          ks_next = key_scale(j + 1);
+        }
+        int cb[BN / 16];
+#pragma unroll
+        for (int b = 0; b < BN / 16; ++b) cb[b] = __shfl_sync(0xffffffffu, coord, b);
+        const int slot = j % ns;
+        if (lane == 0) ok = mbar_wait(bar(be + slot), ((j / ns) & 1) ^ 1, w);
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+        if (is_k) {
+          // Scales of tile j go to slot j mod 2 NK.  The slot's last reader is tile j - 2 NK: this
+          // tile's K slot was freed by QK^T of tile j - NK, which waited for every softmax to have
+          // read S of the tile before it, and so to be done with the scales of all earlier ones.
+          if (lane < 8)
+            *reinterpret_cast<float*>(base_ptr + L::KS_OFF + (j % (2 * NK)) * 32 + lane * 4) = ks;
+          __syncwarp();
+        }
+        if (lane == 0) {
+          const uint32_t dst = dst0 + slot * L::CTILE;
+          mbar_arrive_expect_tx(bar(bf + slot), L::CTILE);
+#pragma unroll
+          for (int b = 0; b < BN / 16; ++b)
+            if (b < nb)
+              tma_load_3d(dst + static_cast<uint32_t>(b * R * D), map, 0, head, cb[b],
+                          bar(bf + slot));
+        }
+        issued = j + 1;
+      }
+      if (lane == 0) {
+        // every load this warp issued must land before shared memory is released
+        for (int r = 0; r < ns && r < issued; ++r) {
+          const int jl = issued - 1 - r;
+          mbar_wait_drain(bar(bf + jl % ns), (jl / ns) & 1);
+        }
+      }
+    } else if (warp >= 12) {
+      // -------------------------------------------------------------------------- V to f16
+      const int key = threadIdx.x - 384;                   // row of the tile this thread converts
+      const int first = kb * BN, last = min((kb + nk) * BN, n_max);
+      // the largest value exponent of this CTA's keys
+      int emax = 0;
+      for (int tok = first + 16 * key; tok < last; tok += 16 * 128)
+        emax = max(emax, static_cast<int>(__ldg(
+                             p.v_scale + static_cast<int64_t>(fp8_row(p, tok) / 16) * p.Hk + head)));
+      emax = __reduce_max_sync(0xffffffffu, emax);
+      int* const em = reinterpret_cast<int*>(base_ptr + L::MISC_OFF + 16);   // one per warp
+      if (lane == 0) em[warp - 12] = emax;
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+      emax = max(max(em[0], em[1]), max(em[2], em[3])) - 127;
+      if (key == 0) {
+        *emax_slot = emax;
+        mbar_arrive(bar(L::B_EM));
+      }
+      auto factor = [&](int t) -> uint32_t {               // 2^(e_v - E + 7) as two f16
+        const int tok = (kb + t) * BN + key / 16 * 16;
+        if (t >= nk || tok >= n_max) return 0u;
+        const int e = static_cast<int>(__ldg(
+                          p.v_scale + static_cast<int64_t>(fp8_row(p, tok) / 16) * p.Hk + head)) -
+                      127 - emax + 7;
+        const uint32_t h = e >= -14 ? static_cast<uint32_t>(e + 15) << 10
+                           : e >= -24 ? 1u << (e + 24) : 0u;
+        return h | (h << 16);
+      };
+      uint32_t f_next = factor(0);
+      bool ok = true;
+      for (int j = 0; j < nk; ++j) {
+        const uint32_t f = f_next;
+        f_next = factor(j + 1);
+        const int cs = j % NC, vs = j % NV;
+        ok = mbar_wait(bar(L::B_CF + cs), (j / NC) & 1, w);
+        if (ok) ok = mbar_wait(bar(L::B_VE + vs), ((j / NV) & 1) ^ 1, w);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        const uint32_t src = base + L::C_OFF + cs * L::CTILE;
+        const uint32_t dst = base + L::V_OFF + vs * L::VTILE;
+        const bool seen = (kb + j) * BN + key < n_max;     // else: zeros, whatever the bytes are
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {
+          const uint4 v = ld_shared_v4(src + swz<D>(key, c));
+          const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+          uint32_t o[8];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            o[2 * i] = seen ? mul_f16x2(widen2(in[i]), f) : 0u;
+            o[2 * i + 1] = seen ? mul_f16x2(widen2_high(in[i]), f) : 0u;
+          }
+          // f16 channels 16 c .. 16 c + 15: pieces 2 c and 2 c + 1 of the 128-byte halves
+          const uint32_t half = dst + static_cast<uint32_t>(c / 4) * L::VHALF;
+          const int c2 = (c % 4) * 2;
+          st_shared_v4(half + swz<128>(key, c2), o[0], o[1], o[2], o[3]);
+          st_shared_v4(half + swz<128>(key, c2 + 1), o[4], o[5], o[6], o[7]);
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(bar(L::B_VF + vs));
+        mbar_arrive(bar(L::B_CE + cs));
+      }
+    } else if (lane == 0) {
+      // ---------------------------------------------------------------------- MMA issuers
+      constexpr uint32_t idesc_qk = idesc_e4m3_f32(kBM, BN);
+      constexpr uint32_t idesc_pv = idesc_f16_f32_bmn(kBM, D);
+      bool ok = true;
+      if (warp == 9) {
+        // S(j, q) = (hi_q + lo_q) K_j^T: 2 D/32 steps of 32 channels into the shared S columns
+        int sf = 0;           // S-free phases consumed
+        ok = mbar_wait(bar(L::B_Q), 0, w);
+        for (int j = 0; ok && j < nk; ++j) {
+          const uint64_t dk =
+              smem_desc_codes<D>(base + L::K_OFF + static_cast<uint32_t>(j % NK) * L::CTILE);
+          ok = mbar_wait(bar(L::B_KF + j % NK), (j / NK) & 1, w);
+          for (int q = 0; ok && q < nq; ++q) {
+            if (j > 0 || q > 0) ok = mbar_wait(bar(L::B_SF), (sf++) & 1, w);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t dq = smem_desc_codes<D>(base + L::Q_OFF + 2u * q * L::QTERM);
+#pragma unroll
+            for (int kk = 0; kk < 2 * (D / 32); ++kk)
+              umma_ss_f8(tmem, dq + ((kk / (D / 32) * L::QTERM + kk % (D / 32) * 32) >> 4),
+                         dk + ((kk % (D / 32) * 32) >> 4), idesc_qk, kk > 0 ? 1u : 0u);
+            umma_commit(bar(L::B_S + q));
+            // a second, plain arrival: it hands on what this thread saw with K_j, the key scales
+            mbar_arrive(bar(L::B_S + q));
+          }
+          if (ok) umma_commit(bar(L::B_KE + j % NK));              // K_j free
+        }
+      } else {
+        // O_q += P_q(j) V_j
+        for (int j = 0; ok && j < nk; ++j) {
+          const uint64_t dv = smem_desc_sw128(
+              base + L::V_OFF + static_cast<uint32_t>(j % NV) * L::VTILE, L::VHALF, 1024);
+          ok = mbar_wait(bar(L::B_VF + j % NV), (j / NV) & 1, w);
+          for (int q = 0; ok && q < nq; ++q) {
+            ok = mbar_wait(bar(L::B_P + q), j & 1, w);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t pa = tmem + 128u + static_cast<uint32_t>(q * 64);
+            const uint32_t od = tmem + 256u + static_cast<uint32_t>(q * D);
+#pragma unroll
+            for (int kk = 0; kk < BN / 16; ++kk)
+              umma_ts(od, pa + 8u * kk, dv + ((kk * 2048u) >> 4), idesc_pv,
+                      (j > 0 || kk > 0) ? 1u : 0u);
+            umma_commit(bar(L::B_O + q));
+          }
+          if (ok) umma_commit(bar(L::B_VE + j % NV));              // V_j free
+        }
+      }
+      // every MMA this thread issued must complete before TMEM is released
+      umma_commit(bar(L::B_DRAIN + (warp - 9)));
+      mbar_wait_drain(bar(L::B_DRAIN + (warp - 9)), 0);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+}  // namespace wfk

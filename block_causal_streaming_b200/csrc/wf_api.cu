@@ -16,6 +16,7 @@
 #include "../../include/wf.h"
 #include "append_kernel.cuh"
 #include "attn_fp8_few_kernel.cuh"
+#include "attn_fp8_kernel.cuh"
 #include "attn_kernel.cuh"
 #include "combine_kernel.cuh"
 #include "fp8_block_kernel.cuh"
@@ -1636,29 +1637,74 @@ int segment_list(const wf_segments_t* seg, SegmentList* out) {
   return WF_OK;
 }
 
-// What a call launches: tiles of 16 mt packed rows, each segment on its own, and key parts.
+// What a call launches.  Few packed rows (query rows x heads of a K/V head's group) in every
+// segment: tiles of 16 mt rows on the matrix instructions that read registers; else row blocks of
+// 256 on the tensor core's own memory.  Segments never share a tile or a row block.
 struct Fp8Plan {
-  int mt = 1, tiles = 0, splits = 1;
-  int tile_end[WF_MAX_CHUNKS];
+  bool few = true;
+  int mt = 1, splits = 1;
+  int tiles = 0;                    // tiles or row blocks
+  int order[WF_MAX_CHUNKS];         // segments in dispatch order
+  int tile_end[WF_MAX_CHUNKS];      // in that order
 };
+
+constexpr int kFewRows = 32;        // packed rows up to which the few-row kernel runs
+
+// Key parts of each row block: the count a model of the grid finds shortest, in times of a key
+// tile.  Blocks go out most keys first, one to an SM at a time; each costs its tiles and about 2.5
+// for its start and end; the join of a split costs about kMergePerPart for a million parts of rows.
+int fp8_row_block_splits(const SegmentList& sl, const Fp8Plan& plan, int Hq, int Hk,
+                         int num_sms) {
+  const int64_t units = static_cast<int64_t>(plan.tiles) * Hk;
+  if (units >= 2 * static_cast<int64_t>(num_sms)) return 1;
+  int best = 1;
+  double best_cost = 0;
+  const int most = (sl.max_kv + wfk::kBN - 1) / wfk::kBN;
+  for (int S = 1; S <= std::min(kMaxSplits, std::max(most, 1)); ++S) {
+    double cost = S > 1 ? kMergePerPart * sl.t_q * Hq * S / 1e6 : 0;
+    int seg = 0;
+    for (int64_t u = 0; u < units * S; u += num_sms) {     // one wave after the other
+      const int64_t block = u / S / Hk;
+      while (block >= plan.tile_end[seg]) ++seg;
+      const int tiles = (sl.kv[plan.order[seg]] + wfk::kBN - 1) / wfk::kBN;
+      cost += (tiles + S - 1) / S + kCtaOverhead;
+    }
+    if (S == 1 || cost < best_cost) {
+      best = S;
+      best_cost = cost;
+    }
+  }
+  return best;
+}
 
 int fp8_plan(const SegmentList& sl, int Hq, int Hk, int splits, int num_sms, Fp8Plan* plan) {
   const int64_t group = Hq / Hk;
   int64_t most = 0, tiles = 0;
-  for (int i = 0; i < sl.n; ++i) most = std::max(most, sl.rows(i) * group);
-  plan->mt = most > 16 ? 2 : 1;
   for (int i = 0; i < sl.n; ++i) {
-    tiles += (sl.rows(i) * group + 16 * plan->mt - 1) / (16 * plan->mt);
+    most = std::max(most, sl.rows(i) * group);
+    plan->order[i] = i;
+  }
+  if (most > INT32_MAX) return WF_ERR_SHAPE;
+  plan->few = most <= kFewRows;
+  plan->mt = most > 16 ? 2 : 1;
+  if (!plan->few)
+    std::stable_sort(plan->order, plan->order + sl.n,
+                     [&](int a, int b) { return sl.kv[a] > sl.kv[b]; });
+  const int64_t per_tile = plan->few ? 16 * plan->mt : kUnitRows;
+  for (int i = 0; i < sl.n; ++i) {
+    tiles += (sl.rows(plan->order[i]) * group + per_tile - 1) / per_tile;
     plan->tile_end[i] = static_cast<int>(std::min<int64_t>(tiles, INT32_MAX));
   }
   if (tiles * Hk * kMaxFp8Splits > INT32_MAX) return WF_ERR_SHAPE;
   plan->tiles = static_cast<int>(tiles);
-  const int blocks = (sl.max_kv + 15) / 16;
-  if (splits == 0) {
+  const int blocks = plan->few ? (sl.max_kv + 15) / 16 : (sl.max_kv + wfk::kBN - 1) / wfk::kBN;
+  if (splits == 0 && plan->few) {
     // enough parts to fill the SMs, but two blocks of keys at least for every warp
     const int64_t want = static_cast<int64_t>(num_sms) * (plan->mt == 1 ? 2 : 1);
     splits = static_cast<int>(std::max<int64_t>(1, want / (tiles * Hk)));
     splits = std::min(splits, blocks / (2 * wfk::kFewWarps));
+  } else if (splits == 0) {
+    splits = fp8_row_block_splits(sl, *plan, Hq, Hk, num_sms);
   }
   plan->splits = std::max(1, std::min({splits, kMaxFp8Splits, blocks}));
   return WF_OK;
@@ -1681,6 +1727,73 @@ int launch_few(const wfk::AttnFewParams& p, cudaStream_t s) {
   }
   const unsigned grid = static_cast<unsigned>(p.tiles) * p.Hk * p.splits;
   kernel<<<grid, wfk::kFewThreads, bytes, s>>>(p);
+  return cudaGetLastError() == cudaSuccess ? WF_OK : WF_ERR_CUDA;
+}
+
+// e4m3 tensor (D, H, rows), row stride H * D bytes, box (D, 1, box_rows), swizzled over D bytes.
+bool encode_codes(CUtensorMap* map, const void* ptr, int D, int H, int64_t rows, int box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(H),
+                              static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(H) * D};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(D), 1u, static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t estr[3] = {1u, 1u, 1u};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(ptr), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+int launch_fp8_blocks(const wfk::AttnFewParams& a, const wf_kv_pool_fp8_block_t* pool,
+                      const SegmentList& sl, const Fp8Plan& plan, const DeviceState* d,
+                      cudaStream_t s) {
+  alignas(64) wfk::AttnFp8Params p;
+  std::memset(&p, 0, sizeof(p));
+  p.box_rows = gcd_int(a.page_size, wfk::kBN);
+  const int64_t total_rows = static_cast<int64_t>(a.num_pages) * a.page_size;
+  if (!encode_codes(&p.tm_k, pool->k_codes, D, a.Hk, total_rows, p.box_rows) ||
+      !encode_codes(&p.tm_v, pool->v_codes, D, a.Hk, total_rows, p.box_rows))
+    return WF_ERR_CUDA;
+  p.q = a.q;
+  p.k_scale = a.k_scale;
+  p.v_scale = a.v_scale;
+  p.page_table = a.page_table;
+  p.out = a.out;
+  p.lse = a.lse;
+  p.part_o = a.part_o;
+  p.part_lse = a.part_lse;
+  p.status = d->status;
+  p.grid_abort = d->abort_word;
+  p.launch_id = g_launch_counter.fetch_add(1);
+  if (p.launch_id == 0) p.launch_id = g_launch_counter.fetch_add(1);
+  p.T_q = a.T_q;
+  p.Hq = a.Hq;
+  p.Hk = a.Hk;
+  p.group = a.group;
+  p.page_size = a.page_size;
+  p.num_pages = a.num_pages;
+  p.total_rows = static_cast<int>(total_rows);
+  p.splits = plan.splits;
+  p.head_group = head_group(a.Hk);
+  p.pairs = plan.tiles;
+  p.sl2 = a.sl2;
+  for (int i = 0; i < sl.n; ++i) {
+    const int g = plan.order[i];
+    p.seg_pair_end[i] = plan.tile_end[i];
+    p.seg_row0[i] = g > 0 ? sl.row_end[g - 1] : 0;
+    p.seg_rows[i] = sl.rows(g);
+    p.seg_kv[i] = sl.kv[g];
+  }
+  auto kernel = wfk::wf_attn_fp8_kernel<D>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           wfk::AttnFp8Smem<D>::ALLOC) != cudaSuccess) {
+    cudaGetLastError();
+    return WF_ERR_CUDA;
+  }
+  const unsigned grid = static_cast<unsigned>(p.pairs) * p.Hk * p.splits;
+  kernel<<<grid, wfk::kFp8AttnThreads, wfk::AttnFp8Smem<D>::ALLOC, s>>>(p);
   return cudaGetLastError() == cudaSuccess ? WF_OK : WF_ERR_CUDA;
 }
 
@@ -1767,8 +1880,13 @@ int wf_attn_forward_fp8_block(const void* q, int num_q_heads,
                                           align256(rows * D * sizeof(float)));
   }
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (D == 128) rc = plan.mt == 1 ? launch_few<128, 1>(p, s) : launch_few<128, 2>(p, s);
-  else rc = plan.mt == 1 ? launch_few<64, 1>(p, s) : launch_few<64, 2>(p, s);
+  if (!plan.few)
+    rc = D == 128 ? launch_fp8_blocks<128>(p, kv_pages, sl, plan, d, s)
+                  : launch_fp8_blocks<64>(p, kv_pages, sl, plan, d, s);
+  else if (D == 128)
+    rc = plan.mt == 1 ? launch_few<128, 1>(p, s) : launch_few<128, 2>(p, s);
+  else
+    rc = plan.mt == 1 ? launch_few<64, 1>(p, s) : launch_few<64, 2>(p, s);
   if (rc || plan.splits == 1) return rc;
   const int64_t threads = static_cast<int64_t>(sl.t_q) * num_q_heads * 32;
   const unsigned blocks =
