@@ -289,6 +289,7 @@ class WavefrontDesc:
                            ctypes.cast(self._off, ctypes.POINTER(ctypes.c_int32)),
                            ctypes.cast(self._stage, ctypes.POINTER(ctypes.c_int32)),
                            int(max_pages_per_seq))
+        self.ref = ctypes.byref(self.c)
         self.chunk_offsets = [int(x) for x in chunk_offsets]
         self.num_ctx_chunks = int(num_ctx_chunks)
 
@@ -416,6 +417,7 @@ class Segments:
         self.c = SegmentsC(n, ctypes.cast(self._rows, ctypes.POINTER(ctypes.c_int32)),
                            ctypes.cast(self._kv, ctypes.POINTER(ctypes.c_int32)),
                            int(num_keys), int(max_pages_per_seq))
+        self.ref = ctypes.byref(self.c)
         self.rows_end = [int(x) for x in rows_end]
         self.kv_end = [int(x) for x in kv_end]
         self.num_keys = int(num_keys)
@@ -966,75 +968,89 @@ class NormRope:
         self.ref = ctypes.byref(self.c)
 
 
-def _check_cuda(t, name: str):
-    if not t.is_cuda:
-        raise ValueError(f"{name}: expected a CUDA tensor")
+# A call for one token is a few microseconds on the device, so these checks read every attribute of
+# a tensor once and build nothing they do not pass on.
+_torch = None
 
 
-def _check_one_device(stream, *tensors):
-    """Every tensor on the device the launch goes to: the current one."""
-    import torch
-    here = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != here:
-            raise ValueError(f"a tensor on {t.device}, the current device is {here}")
+def _lib_torch():
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
 
 
-def _rows_arg(t, name: str, L: int, H: int, D: int):
-    """(pointer, token stride) of a bf16 [L, H, D] tensor whose heads lie together."""
-    import torch
-    if tuple(t.shape) != (L, H, D):
+def _current_device() -> int:
+    return _lib_torch()._C._cuda_getDevice()
+
+
+def _raw_stream(stream, device: int):
+    """Handle of ``stream``, or of the current stream of the current device."""
+    if stream is None:
+        return _torch._C._cuda_getCurrentRawStream(device)
+    return getattr(stream, "cuda_stream", stream)
+
+
+def _ptr(t, name: str, dtype, device: int) -> int:
+    """Address of a contiguous tensor of ``dtype`` on the device the launch goes to."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.get_device() != device:
+        raise ValueError(f"{name}: expected a tensor on the current CUDA device ({device}), got one "
+                         f"on {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor")
+    return t.data_ptr()
+
+
+def _rows_arg(t, name: str, L: int, H: int, D: int, device: int):
+    """(address, token stride) of a bf16 [L, H, D] tensor whose heads lie together."""
+    if t.shape != (L, H, D):
         raise ValueError(f"{name}: expected [{L}, {H}, {D}], got {tuple(t.shape)}")
-    if t.dtype is not torch.bfloat16:
+    if t.dtype is not _torch.bfloat16:
         raise TypeError(f"{name}: expected torch.bfloat16, got {t.dtype}")
-    _check_cuda(t, name)
-    s0, s1, s2 = t.stride()
-    if L * H * D == 0:
+    if t.get_device() != device:
+        raise ValueError(f"{name}: expected a tensor on the current CUDA device ({device}), got one "
+                         f"on {t.device}")
+    if L == 0 or H == 0:
         return None, H * D
-    if s2 != 1 or (H > 1 and s1 != D):
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (s1 != D and H > 1):
         raise ValueError(f"{name}: every token's [{H}, {D}] must be contiguous, strides "
-                         f"{tuple(t.stride())}")
-    if L > 1 and (s0 < H * D or s0 % 8):
+                         f"{t.stride()}")
+    if L == 1:
+        return t.data_ptr(), H * D
+    if s0 < H * D or s0 % 8:
         raise ValueError(f"{name}: the stride from token to token must be a multiple of 8 and at "
                          f"least {H * D}, got {s0}")
-    return t.data_ptr(), s0 if L > 1 else H * D
+    return t.data_ptr(), s0
 
 
-def _weight_arg(w, name: str, rule: Optional[NormRope], H: int, D: int):
+def _weight_arg(w, name: str, rule: Optional[NormRope], H: int, D: int, device: int):
     if w is None:
         return None
-    want = (H, D) if rule is not None and rule.weight_per_head else (D,)
-    if tuple(w.shape) != want:
-        raise ValueError(f"{name}: expected {list(want)}, got {tuple(w.shape)}")
     if rule is None or not rule.norm:
         raise ValueError(f"{name}: a weight without a norm")
-    _check_tensor(w, name, "bf16")
-    return w.data_ptr()
+    if w.shape != ((H, D) if rule.weight_per_head else (D,)):
+        raise ValueError(f"{name}: expected {[H, D] if rule.weight_per_head else [D]}, got "
+                         f"{tuple(w.shape)}")
+    return _ptr(w, name, _torch.bfloat16, device)
 
 
-def _positions_arg(positions, rule: Optional[NormRope], L: int, D: int):
+def _positions_arg(positions, rule: Optional[NormRope], L: int, D: int, device: int):
     if rule is None or rule.table is None:
         if positions is not None:
             raise ValueError("positions: the rule has no rotation")
         return None
     if rule.pairs * 2 > D:
         raise ValueError(f"table: {rule.pairs} pairs in rows of {D} values")
-    if positions is None or tuple(positions.shape) != (L, rule.num_axes):
+    if rule.table.get_device() != device:
+        raise ValueError(f"table: on {rule.table.device}, the current CUDA device is {device}")
+    if positions is None or positions.shape != (L, rule.num_axes):
         raise ValueError(f"positions: expected [{L}, {rule.num_axes}], got "
                          f"{None if positions is None else tuple(positions.shape)}")
-    _check_tensor(positions, "positions", "i32")
-    return positions.data_ptr()
-
-
-def _overlap(a, b) -> bool:
-    """Whether two tensors' spans of memory meet."""
-    def span(t):
-        n = sum((int(x) - 1) * int(y) for x, y in zip(t.shape, t.stride())) + 1
-        return t.data_ptr(), t.data_ptr() + n * t.element_size()
-    if a.numel() == 0 or b.numel() == 0:
-        return False
-    (a0, a1), (b0, b1) = span(a), span(b)
-    return a0 < b1 and b0 < a1
+    return _ptr(positions, "positions", _torch.int32, device)
 
 
 def qk_norm_rope(q, q_out, k, k_out, rule: NormRope, positions=None, q_weight=None,
@@ -1042,55 +1058,60 @@ def qk_norm_rope(q, q_out, k, k_out, rule: NormRope, positions=None, q_weight=No
     """wf_qk_norm_rope: norm and rotation of ``q`` ([T, Hq, D] bf16, tokens may be strided) into
     ``q_out`` and, in the same launch, of ``k`` into ``k_out`` (both None: queries only).
     ``positions``: int32 [T, axes].  The outputs are contiguous; an output may be its own input."""
-    if q.dim() != 3:
+    device = _current_device()
+    if len(q.shape) != 3:
         raise ValueError(f"q: expected [T, H, D], got {tuple(q.shape)}")
-    L, Hq, D = (int(x) for x in q.shape)
-    qp, qs = _rows_arg(q, "q", L, Hq, D)
-    Hk, kp, ks, kop = 0, None, 0, None
-    if tuple(q_out.shape) != (L, Hq, D):
+    L, Hq, D = q.shape
+    qp, qs = _rows_arg(q, "q", L, Hq, D, device)
+    if q_out.shape != q.shape:
         raise ValueError(f"q_out: expected [{L}, {Hq}, {D}], got {tuple(q_out.shape)}")
-    _check_tensor(q_out, "q_out", "bf16")
-    outs = [(q_out, "q_out", q)]
-    if (k is None) != (k_out is None):
-        raise ValueError("k and k_out go together")
+    qo = _ptr(q_out, "q_out", _torch.bfloat16, device)
+    Hk, kp, ks, ko = 0, None, 0, None
     if k is not None:
-        if k.dim() != 3:
-            raise ValueError(f"k: expected [T, H, D], got {tuple(k.shape)}")
-        Hk = int(k.shape[1])
-        kp, ks = _rows_arg(k, "k", L, Hk, D)
-        if tuple(k_out.shape) != (L, Hk, D):
-            raise ValueError(f"k_out: expected [{L}, {Hk}, {D}], got {tuple(k_out.shape)}")
-        _check_tensor(k_out, "k_out", "bf16")
-        kop = k_out.data_ptr()
-        outs.append((k_out, "k_out", k))
-        if _overlap(q_out, k_out):
-            raise ValueError("q_out and k_out overlap")
-    for o, n, own_in in outs:
-        for x in (q, k):
-            if x is None or (x is own_in and x.is_contiguous()):
-                continue
-            if _overlap(o, x) and not (x is own_in and x.data_ptr() == o.data_ptr() and
-                                       x.stride() == o.stride()):
-                raise ValueError(f"{n} overlaps an input (only its own, contiguous, may be the "
-                                 "same memory)")
-    qw = _weight_arg(q_weight, "q_weight", rule, Hq, D)
-    kw = _weight_arg(k_weight, "k_weight", rule, Hk, D)
-    pp = _positions_arg(positions, rule, L, D)
-    _check_one_device(stream, q, q_out, k, k_out, q_weight, k_weight, positions, rule.table)
-    rc = lib.wf_qk_norm_rope(qp, qs, q_out.data_ptr(), qw, Hq, kp, ks, kop, kw, Hk, L, D, pp,
-                             rule.ref, _stream_handle(stream))
+        if k_out is None or len(k.shape) != 3 or k_out.shape != k.shape:
+            raise ValueError(f"k, k_out: expected the same [{L}, H, {D}], got {tuple(k.shape)} and "
+                             f"{None if k_out is None else tuple(k_out.shape)}")
+        Hk = k.shape[1]
+        kp, ks = _rows_arg(k, "k", L, Hk, D, device)
+        ko = _ptr(k_out, "k_out", _torch.bfloat16, device)
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    if L > 0 and Hq > 0:
+        # [begin, end) of every tensor's memory: an output may meet nothing but its own input, and
+        # that only where it is the same contiguous rows
+        qe, qoe = qp + 2 * ((L - 1) * qs + Hq * D), qo + 2 * L * Hq * D
+        if qo < qe and qp < qoe and not (qo == qp and qs == Hq * D):
+            raise ValueError("q_out overlaps q")
+        if Hk > 0:
+            ke, koe = kp + 2 * ((L - 1) * ks + Hk * D), ko + 2 * L * Hk * D
+            if ko < ke and kp < koe and not (ko == kp and ks == Hk * D):
+                raise ValueError("k_out overlaps k")
+            if (qo < ke and kp < qoe) or (ko < qe and qp < koe) or (qo < koe and ko < qoe):
+                raise ValueError("q_out or k_out overlaps the other's rows")
+    qw = _weight_arg(q_weight, "q_weight", rule, Hq, D, device)
+    kw = _weight_arg(k_weight, "k_weight", rule, Hk, D, device)
+    pp = _positions_arg(positions, rule, L, D, device)
+    rc = lib.wf_qk_norm_rope(qp, qs, qo, qw, Hq, kp, ks, ko, kw, Hk, L, D, pp, rule.ref,
+                             _raw_stream(stream, device))
     if rc != WF_OK:
         raise WfError(rc, "wf_qk_norm_rope")
 
 
-def _append_rows(k, v, chunk_begin: int, chunk_end: int, wf: WavefrontDesc, H: int, D: int):
-    """Pointers and strides of an append's rows, and their count."""
+def _append_len(chunk_begin: int, chunk_end: int, wf: WavefrontDesc) -> int:
     off = wf.chunk_offsets
-    if not 0 <= int(chunk_begin) < int(chunk_end) <= len(off) - 1:
+    if not 0 <= chunk_begin < chunk_end < len(off):
         raise ValueError(f"chunks [{chunk_begin}, {chunk_end}) outside the wavefront's "
                          f"{len(off) - 1}")
-    L = off[chunk_end] - off[chunk_begin]
-    return (L,) + _rows_arg(k, "k", L, H, D) + _rows_arg(v, "v", L, H, D)
+    return off[chunk_end] - off[chunk_begin]
+
+
+def _page_table_arg(page_table, layer: int, wf: WavefrontDesc, device: int):
+    if len(page_table.shape) != 2 or page_table.shape[1] != wf.c.max_pages_per_seq:
+        raise ValueError(f"page_table: expected [num_layers, {wf.c.max_pages_per_seq}], got "
+                         f"{tuple(page_table.shape)}")
+    if not 0 <= layer < page_table.shape[0]:
+        raise ValueError(f"layer {layer} outside the page table's {page_table.shape[0]} rows")
+    return _ptr(page_table, "page_table", _torch.int32, device)
 
 
 def kv_append_rope(k_pool, v_pool, layer: int, chunk_begin: int, chunk_end: int, k, v, page_table,
@@ -1098,34 +1119,38 @@ def kv_append_rope(k_pool, v_pool, layer: int, chunk_begin: int, chunk_end: int,
                    stream=None) -> None:
     """wf_kv_append_rope: chunks [chunk_begin, chunk_end) into the bf16 pools, keys normed and
     rotated on the way.  ``k``, ``v``: those chunks' rows, [L, H, D] bf16, tokens may be strided."""
-    num_pages, page_size, H, D = _pool_shape(k_pool, v_pool)
-    L, kp, ks, vp, vs = _append_rows(k, v, chunk_begin, chunk_end, wf, H, D)
-    _check_page_table(page_table, layer, wf)
-    _check_tensor(k_pool, "k_pool", "bf16")
-    _check_tensor(v_pool, "v_pool", "bf16")
-    _check_tensor(page_table, "page_table", "i32")
-    kw = _weight_arg(k_weight, "k_weight", rule, H, D)
-    pp = _positions_arg(positions, rule, L, D)
-    _check_one_device(stream, k_pool, v_pool, k, v, page_table, k_weight, positions, rule.table)
-    pool = KvPool(k_pool.data_ptr(), v_pool.data_ptr(), num_pages, page_size, H, D)
-    rc = lib.wf_kv_append_rope(ctypes.byref(pool), int(layer), int(chunk_begin), int(chunk_end),
-                               kp, ks, vp, vs, kw, pp, rule.ref, page_table.data_ptr(),
-                               ctypes.byref(wf.c), _stream_handle(stream))
+    device = _current_device()
+    if len(k_pool.shape) != 4 or v_pool.shape != k_pool.shape:
+        raise ValueError("pool: K and V must both be [num_pages, page_size, H, D], got "
+                         f"{tuple(k_pool.shape)} and {tuple(v_pool.shape)}")
+    num_pages, page_size, H, D = k_pool.shape
+    L = _append_len(chunk_begin, chunk_end, wf)
+    kp, ks = _rows_arg(k, "k", L, H, D, device)
+    vp, vs = _rows_arg(v, "v", L, H, D, device)
+    pool = KvPool(_ptr(k_pool, "k_pool", _torch.bfloat16, device),
+                  _ptr(v_pool, "v_pool", _torch.bfloat16, device), num_pages, page_size, H, D)
+    pt = _page_table_arg(page_table, layer, wf, device)
+    kw = _weight_arg(k_weight, "k_weight", rule, H, D, device)
+    pp = _positions_arg(positions, rule, L, D, device)
+    rc = lib.wf_kv_append_rope(ctypes.byref(pool), layer, chunk_begin, chunk_end, kp, ks, vp, vs,
+                               kw, pp, rule.ref, pt, wf.ref, _raw_stream(stream, device))
     if rc != WF_OK:
         raise WfError(rc, "wf_kv_append_rope")
 
 
-def _fp8_block_pool(k_codes, v_codes, k_scale, v_scale) -> KvPoolFp8Block:
-    num_pages, page_size, H, D = _pool_shape(k_codes, v_codes, "FP8 cache codes")
+def _fp8_block_pool(k_codes, v_codes, k_scale, v_scale, device: int) -> KvPoolFp8Block:
+    if len(k_codes.shape) != 4 or v_codes.shape != k_codes.shape:
+        raise ValueError("FP8 cache: K and V codes must both be [num_pages, page_size, H, D], got "
+                         f"{tuple(k_codes.shape)} and {tuple(v_codes.shape)}")
+    num_pages, page_size, H, D = k_codes.shape
     want = (num_pages, page_size // 16, H)
-    if tuple(k_scale.shape) != want or tuple(v_scale.shape) != want:
+    if k_scale.shape != want or v_scale.shape != want:
         raise ValueError(f"FP8 cache: scales must be {list(want)} (pages, page_size / 16, H), got "
                          f"{tuple(k_scale.shape)} and {tuple(v_scale.shape)}")
-    for t, n in ((k_codes, "k_codes"), (v_codes, "v_codes"), (k_scale, "k_scale"),
-                 (v_scale, "v_scale")):
-        _check_tensor(t, n, "u8")
-    return KvPoolFp8Block(k_codes.data_ptr(), v_codes.data_ptr(), k_scale.data_ptr(),
-                          v_scale.data_ptr(), num_pages, page_size, H, D)
+    u8 = _torch.uint8
+    return KvPoolFp8Block(_ptr(k_codes, "k_codes", u8, device), _ptr(v_codes, "v_codes", u8, device),
+                          _ptr(k_scale, "k_scale", u8, device), _ptr(v_scale, "v_scale", u8, device),
+                          num_pages, page_size, H, D)
 
 
 def kv_append_fp8_block(k_codes, v_codes, k_scale, v_scale, layer: int, chunk_begin: int,
@@ -1135,20 +1160,18 @@ def kv_append_fp8_block(k_codes, v_codes, k_scale, v_scale, layer: int, chunk_be
     """wf_kv_append_fp8_block: chunks [chunk_begin, chunk_end) into an FP8 cache (uint8 e4m3 codes
     [pages, page_size, H, D], uint8 e8m0 scales [pages, page_size / 16, H]; zeroed at first), keys
     normed and rotated on the way when ``rule`` is given."""
-    pool = _fp8_block_pool(k_codes, v_codes, k_scale, v_scale)
+    device = _current_device()
+    pool = _fp8_block_pool(k_codes, v_codes, k_scale, v_scale, device)
     H, D = pool.num_heads, pool.head_dim
-    L, kp, ks, vp, vs = _append_rows(k, v, chunk_begin, chunk_end, wf, H, D)
-    _check_page_table(page_table, layer, wf)
-    _check_tensor(page_table, "page_table", "i32")
-    kw = _weight_arg(k_weight, "k_weight", rule, H, D)
-    pp = _positions_arg(positions, rule, L, D)
-    _check_one_device(stream, k_codes, v_codes, k_scale, v_scale, k, v, page_table, k_weight,
-                      positions, rule.table if rule is not None else None)
-    rc = lib.wf_kv_append_fp8_block(ctypes.byref(pool), int(layer), int(chunk_begin),
-                                    int(chunk_end), kp, ks, vp, vs, kw, pp,
-                                    rule.ref if rule is not None else None,
-                                    page_table.data_ptr(), ctypes.byref(wf.c),
-                                    _stream_handle(stream))
+    L = _append_len(chunk_begin, chunk_end, wf)
+    kp, ks = _rows_arg(k, "k", L, H, D, device)
+    vp, vs = _rows_arg(v, "v", L, H, D, device)
+    pt = _page_table_arg(page_table, layer, wf, device)
+    kw = _weight_arg(k_weight, "k_weight", rule, H, D, device)
+    pp = _positions_arg(positions, rule, L, D, device)
+    rc = lib.wf_kv_append_fp8_block(ctypes.byref(pool), layer, chunk_begin, chunk_end, kp, ks, vp,
+                                    vs, kw, pp, rule.ref if rule is not None else None, pt,
+                                    wf.ref, _raw_stream(stream, device))
     if rc != WF_OK:
         raise WfError(rc, "wf_kv_append_fp8_block")
 
@@ -1167,33 +1190,28 @@ def attn_forward_fp8_block(q, k_codes, v_codes, k_scale, v_scale, page_table_row
     """wf_attn_forward_fp8_block: rows of segment i of ``q`` ([T, Hq, D] bf16) see logical keys
     [0, kv_end[i]) of an FP8 cache (see :func:`kv_append_fp8_block`) whose H heads each serve
     Hq / H query heads; ``lse``: fp32 [Hq, T]."""
-    pool = _fp8_block_pool(k_codes, v_codes, k_scale, v_scale)
+    device = _current_device()
+    pool = _fp8_block_pool(k_codes, v_codes, k_scale, v_scale, device)
     t_q = seg.t_q
-    if q.dim() != 3 or int(q.shape[0]) != t_q or int(q.shape[2]) != pool.head_dim or \
-            int(q.shape[1]) % pool.num_heads or q.shape[1] == 0:
+    if len(q.shape) != 3 or q.shape[0] != t_q or q.shape[2] != pool.head_dim or \
+            q.shape[1] % max(pool.num_heads, 1) or q.shape[1] == 0:
         raise ValueError(f"q: expected [{t_q}, a multiple of {pool.num_heads}, {pool.head_dim}], "
                          f"got {tuple(q.shape)}")
-    if tuple(out.shape) != tuple(q.shape):
+    if out.shape != q.shape:
         raise ValueError(f"out: expected {tuple(q.shape)}, got {tuple(out.shape)}")
-    Hq = int(q.shape[1])
-    _check_tensor(q, "q", "bf16")
-    _check_tensor(out, "out", "bf16")
-    _check_tensor(page_table_row, "page_table_row", "i32")
-    if page_table_row.dim() != 1 or page_table_row.numel() < seg.c.max_pages_per_seq:
+    Hq = q.shape[1]
+    if len(page_table_row.shape) != 1 or page_table_row.shape[0] < seg.c.max_pages_per_seq:
         raise ValueError(f"page_table_row: needs {seg.c.max_pages_per_seq} entries")
-    if lse is not None:
-        if tuple(lse.shape) != (Hq, t_q):
-            raise ValueError(f"lse: expected [{Hq}, {t_q}], got {tuple(lse.shape)}")
-        _check_tensor(lse, "lse", "f32")
-    if workspace is not None:
-        _check_tensor(workspace, "workspace", "u8")
-    _check_one_device(stream, q, out, k_codes, v_codes, k_scale, v_scale, page_table_row, lse,
-                      workspace)
+    if lse is not None and lse.shape != (Hq, t_q):
+        raise ValueError(f"lse: expected [{Hq}, {t_q}], got {tuple(lse.shape)}")
+    bf16 = _torch.bfloat16
     rc = lib.wf_attn_forward_fp8_block(
-        q.data_ptr(), Hq, ctypes.byref(pool), page_table_row.data_ptr(), ctypes.byref(seg.c),
-        float(scale), out.data_ptr(), lse.data_ptr() if lse is not None else None, int(splits),
-        workspace.data_ptr() if workspace is not None else None,
-        workspace.numel() if workspace is not None else 0, _stream_handle(stream))
+        _ptr(q, "q", bf16, device), Hq, ctypes.byref(pool),
+        _ptr(page_table_row, "page_table_row", _torch.int32, device), seg.ref, scale,
+        _ptr(out, "out", bf16, device),
+        None if lse is None else _ptr(lse, "lse", _torch.float32, device), splits,
+        None if workspace is None else _ptr(workspace, "workspace", _torch.uint8, device),
+        0 if workspace is None else workspace.numel(), _raw_stream(stream, device))
     if rc != WF_OK:
         raise WfError(rc, "wf_attn_forward_fp8_block")
 

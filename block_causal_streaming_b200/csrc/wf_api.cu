@@ -94,7 +94,25 @@ int device_state(DeviceState** out) {
                                  wfk::AttnSmem<128, true>::ALLOC) != cudaSuccess ||
             cudaFuncSetAttribute(wfk::wf_attn_fwd_kernel<128, false, true, true>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 wfk::AttnSmem<128, true>::ALLOC) != cudaSuccess) {
+                                 wfk::AttnSmem<128, true>::ALLOC) != cudaSuccess ||
+            cudaFuncSetAttribute(wfk::wf_attn_fp8_kernel<128>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 wfk::AttnFp8Smem<128>::ALLOC) != cudaSuccess ||
+            cudaFuncSetAttribute(wfk::wf_attn_fp8_kernel<64>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 wfk::AttnFp8Smem<64>::ALLOC) != cudaSuccess ||
+            cudaFuncSetAttribute(wfk::wf_attn_fp8_few_kernel<128, 1>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 wfk::FewSmem<128, 1>::BYTES) != cudaSuccess ||
+            cudaFuncSetAttribute(wfk::wf_attn_fp8_few_kernel<128, 2>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 wfk::FewSmem<128, 2>::BYTES) != cudaSuccess ||
+            cudaFuncSetAttribute(wfk::wf_attn_fp8_few_kernel<64, 1>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 wfk::FewSmem<64, 1>::BYTES) != cudaSuccess ||
+            cudaFuncSetAttribute(wfk::wf_attn_fp8_few_kernel<64, 2>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 wfk::FewSmem<64, 2>::BYTES) != cudaSuccess) {
           cudaGetLastError();
           return WF_ERR_CUDA;
         }
@@ -1720,11 +1738,6 @@ template <int D, int MT>
 int launch_few(const wfk::AttnFewParams& p, cudaStream_t s) {
   auto kernel = wfk::wf_attn_fp8_few_kernel<D, MT>;
   const int bytes = static_cast<int>(wfk::FewSmem<D, MT>::BYTES);
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
-      cudaSuccess) {
-    cudaGetLastError();
-    return WF_ERR_CUDA;
-  }
   const unsigned grid = static_cast<unsigned>(p.tiles) * p.Hk * p.splits;
   kernel<<<grid, wfk::kFewThreads, bytes, s>>>(p);
   return cudaGetLastError() == cudaSuccess ? WF_OK : WF_ERR_CUDA;
@@ -1787,11 +1800,6 @@ int launch_fp8_blocks(const wfk::AttnFewParams& a, const wf_kv_pool_fp8_block_t*
     p.seg_kv[i] = sl.kv[g];
   }
   auto kernel = wfk::wf_attn_fp8_kernel<D>;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           wfk::AttnFp8Smem<D>::ALLOC) != cudaSuccess) {
-    cudaGetLastError();
-    return WF_ERR_CUDA;
-  }
   const unsigned grid = static_cast<unsigned>(p.pairs) * p.Hk * p.splits;
   kernel<<<grid, wfk::kFp8AttnThreads, wfk::AttnFp8Smem<D>::ALLOC, s>>>(p);
   return cudaGetLastError() == cudaSuccess ? WF_OK : WF_ERR_CUDA;
