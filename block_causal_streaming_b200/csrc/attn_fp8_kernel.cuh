@@ -104,13 +104,6 @@ struct AttnFp8Smem {
   static_assert(ALLOC <= 227u * 1024u, "shared memory per CTA exceeds 227 KB");
 };
 
-// Offset of 16-byte piece c of row r in a tile of D-byte rows under the D-byte swizzle.
-template <int D>
-__device__ __forceinline__ uint32_t swz(int r, int c) {
-  return D == 128 ? static_cast<uint32_t>(r * 128 + ((c ^ (r & 7)) * 16))
-                  : static_cast<uint32_t>(r * 64 + ((c ^ ((r >> 1) & 3)) * 16));
-}
-
 // Shared-memory matrix descriptor of a K-major tile of D-byte rows under the D-byte swizzle.
 template <int D>
 __device__ __forceinline__ uint64_t smem_desc_codes(uint32_t start) {
@@ -141,29 +134,10 @@ __device__ __forceinline__ void st_shared_v4(uint32_t a, uint32_t x, uint32_t y,
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w)
                : "memory");
 }
-__device__ __forceinline__ uint4 ld_shared_v4(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(a)
-               : "memory");
-  return v;
-}
 __device__ __forceinline__ float4 ld_shared_f4(uint32_t a) {
   const uint4 v = ld_shared_v4(a);
   return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z),
                      __uint_as_float(v.w));
-}
-
-// Pool row of logical token `tok`; a page outside the pool is recorded and read as page 0.
-__device__ __forceinline__ int fp8_row(const AttnFp8Params& p, int tok) {
-  const int idx = tok / p.page_size;
-  int pg = __ldg(p.page_table + idx);
-  if (pg < 0 || pg >= p.num_pages) {
-    atomicCAS(p.status, 0, 5 /* WF_ERR_PAGE_OOB */);
-    pg = 0;
-  }
-  return pg * p.page_size + (tok - idx * p.page_size);
 }
 
 template <int D>

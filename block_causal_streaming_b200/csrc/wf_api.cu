@@ -103,16 +103,22 @@ int device_state(DeviceState** out) {
                                  wfk::AttnFp8Smem<64>::ALLOC) != cudaSuccess ||
             cudaFuncSetAttribute(wfk::wf_attn_fp8_few_kernel<128, 1>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 wfk::FewSmem<128, 1>::BYTES) != cudaSuccess ||
+                                 wfk::FewSmem<128, 1>::ALLOC) != cudaSuccess ||
             cudaFuncSetAttribute(wfk::wf_attn_fp8_few_kernel<128, 2>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 wfk::FewSmem<128, 2>::BYTES) != cudaSuccess ||
+                                 wfk::FewSmem<128, 2>::ALLOC) != cudaSuccess ||
+            cudaFuncSetAttribute(wfk::wf_attn_fp8_few_kernel<128, 4>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 wfk::FewSmem<128, 4>::ALLOC) != cudaSuccess ||
             cudaFuncSetAttribute(wfk::wf_attn_fp8_few_kernel<64, 1>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 wfk::FewSmem<64, 1>::BYTES) != cudaSuccess ||
+                                 wfk::FewSmem<64, 1>::ALLOC) != cudaSuccess ||
             cudaFuncSetAttribute(wfk::wf_attn_fp8_few_kernel<64, 2>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 wfk::FewSmem<64, 2>::BYTES) != cudaSuccess) {
+                                 wfk::FewSmem<64, 2>::ALLOC) != cudaSuccess ||
+            cudaFuncSetAttribute(wfk::wf_attn_fp8_few_kernel<64, 4>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 wfk::FewSmem<64, 4>::ALLOC) != cudaSuccess) {
           cudaGetLastError();
           return WF_ERR_CUDA;
         }
@@ -1656,11 +1662,11 @@ int segment_list(const wf_segments_t* seg, SegmentList* out) {
 }
 
 // What a call launches.  Few packed rows (query rows x heads of a K/V head's group) in every
-// segment: tiles of 16 mt rows on the matrix instructions that read registers; else row blocks of
+// segment: tiles of 8 nt rows on the matrix instructions that read registers; else row blocks of
 // 256 on the tensor core's own memory.  Segments never share a tile or a row block.
 struct Fp8Plan {
   bool few = true;
-  int mt = 1, splits = 1;
+  int nt = 1, splits = 1;
   int tiles = 0;                    // tiles or row blocks
   int order[WF_MAX_CHUNKS];         // segments in dispatch order
   int tile_end[WF_MAX_CHUNKS];      // in that order
@@ -1704,23 +1710,24 @@ int fp8_plan(const SegmentList& sl, int Hq, int Hk, int splits, int num_sms, Fp8
   }
   if (most > INT32_MAX) return WF_ERR_SHAPE;
   plan->few = most <= kFewRows;
-  plan->mt = most > 16 ? 2 : 1;
+  plan->nt = most > 16 ? 4 : most > 8 ? 2 : 1;
   if (!plan->few)
     std::stable_sort(plan->order, plan->order + sl.n,
                      [&](int a, int b) { return sl.kv[a] > sl.kv[b]; });
-  const int64_t per_tile = plan->few ? 16 * plan->mt : kUnitRows;
+  const int64_t per_tile = plan->few ? 8 * plan->nt : kUnitRows;
   for (int i = 0; i < sl.n; ++i) {
     tiles += (sl.rows(plan->order[i]) * group + per_tile - 1) / per_tile;
     plan->tile_end[i] = static_cast<int>(std::min<int64_t>(tiles, INT32_MAX));
   }
   if (tiles * Hk * kMaxFp8Splits > INT32_MAX) return WF_ERR_SHAPE;
   plan->tiles = static_cast<int>(tiles);
-  const int blocks = plan->few ? (sl.max_kv + 15) / 16 : (sl.max_kv + wfk::kBN - 1) / wfk::kBN;
+  // parts are runs of 16 keys, or of 128; a part keeps a block for every warp
+  const int blocks = plan->few ? (sl.max_kv + 16 * wfk::kFewWarps - 1) / (16 * wfk::kFewWarps)
+                               : (sl.max_kv + wfk::kBN - 1) / wfk::kBN;
   if (splits == 0 && plan->few) {
-    // enough parts to fill the SMs, but two blocks of keys at least for every warp
-    const int64_t want = static_cast<int64_t>(num_sms) * (plan->mt == 1 ? 2 : 1);
-    splits = static_cast<int>(std::max<int64_t>(1, want / (tiles * Hk)));
-    splits = std::min(splits, blocks / (2 * wfk::kFewWarps));
+    // as many parts as there are places for CTAs (two an SM, one with more than 16 rows)
+    const int64_t places = static_cast<int64_t>(num_sms) * (plan->nt <= 2 ? 2 : 1);
+    splits = static_cast<int>(std::max<int64_t>(1, places / (tiles * Hk)));
   } else if (splits == 0) {
     splits = fp8_row_block_splits(sl, *plan, Hq, Hk, num_sms);
   }
@@ -1734,13 +1741,33 @@ size_t fp8_workspace_bytes(const SegmentList& sl, const Fp8Plan& plan, int Hq, i
   return align256(rows * D * sizeof(float)) + align256(rows * sizeof(float));
 }
 
-template <int D, int MT>
+template <int D, int NT>
 int launch_few(const wfk::AttnFewParams& p, cudaStream_t s) {
-  auto kernel = wfk::wf_attn_fp8_few_kernel<D, MT>;
-  const int bytes = static_cast<int>(wfk::FewSmem<D, MT>::BYTES);
   const unsigned grid = static_cast<unsigned>(p.tiles) * p.Hk * p.splits;
-  kernel<<<grid, wfk::kFewThreads, bytes, s>>>(p);
+  wfk::wf_attn_fp8_few_kernel<D, NT><<<grid, wfk::kFewThreads, wfk::FewSmem<D, NT>::ALLOC, s>>>(p);
   return cudaGetLastError() == cudaSuccess ? WF_OK : WF_ERR_CUDA;
+}
+
+// The join of the few-row kernel's parts, its blocks launched while that kernel still runs.
+template <int D>
+int launch_join(const wfk::AttnFewParams& p, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.T_q) * p.Hq);
+  cfg.blockDim = dim3(wfk::kJoinThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  static_assert(kMaxFp8Splits <= wfk::kMaxJoin, "parts");
+  if (cudaLaunchKernelEx(&cfg, wfk::wf_join_kernel<D>, static_cast<const float*>(p.part_o),
+                         static_cast<const float*>(p.part_lse), p.splits, p.T_q, p.Hq, p.out,
+                         p.lse) != cudaSuccess) {
+    cudaGetLastError();
+    return WF_ERR_CUDA;
+  }
+  return WF_OK;
 }
 
 // e4m3 tensor (D, H, rows), row stride H * D bytes, box (D, 1, box_rows), swizzled over D bytes.
@@ -1759,16 +1786,14 @@ bool encode_codes(CUtensorMap* map, const void* ptr, int D, int H, int64_t rows,
 }
 
 template <int D>
-int launch_fp8_blocks(const wfk::AttnFewParams& a, const wf_kv_pool_fp8_block_t* pool,
-                      const SegmentList& sl, const Fp8Plan& plan, const DeviceState* d,
+int launch_fp8_blocks(const wfk::AttnFewParams& a, const SegmentList& sl, const Fp8Plan& plan,
                       cudaStream_t s) {
   alignas(64) wfk::AttnFp8Params p;
   std::memset(&p, 0, sizeof(p));
-  p.box_rows = gcd_int(a.page_size, wfk::kBN);
-  const int64_t total_rows = static_cast<int64_t>(a.num_pages) * a.page_size;
-  if (!encode_codes(&p.tm_k, pool->k_codes, D, a.Hk, total_rows, p.box_rows) ||
-      !encode_codes(&p.tm_v, pool->v_codes, D, a.Hk, total_rows, p.box_rows))
-    return WF_ERR_CUDA;
+  p.tm_k = a.tm_k;
+  p.tm_v = a.tm_v;
+  p.box_rows = a.box_rows;
+  p.total_rows = a.total_rows;
   p.q = a.q;
   p.k_scale = a.k_scale;
   p.v_scale = a.v_scale;
@@ -1777,17 +1802,15 @@ int launch_fp8_blocks(const wfk::AttnFewParams& a, const wf_kv_pool_fp8_block_t*
   p.lse = a.lse;
   p.part_o = a.part_o;
   p.part_lse = a.part_lse;
-  p.status = d->status;
-  p.grid_abort = d->abort_word;
-  p.launch_id = g_launch_counter.fetch_add(1);
-  if (p.launch_id == 0) p.launch_id = g_launch_counter.fetch_add(1);
+  p.status = a.status;
+  p.grid_abort = a.grid_abort;
+  p.launch_id = a.launch_id;
   p.T_q = a.T_q;
   p.Hq = a.Hq;
   p.Hk = a.Hk;
   p.group = a.group;
   p.page_size = a.page_size;
   p.num_pages = a.num_pages;
-  p.total_rows = static_cast<int>(total_rows);
   p.splits = plan.splits;
   p.head_group = head_group(a.Hk);
   p.pairs = plan.tiles;
@@ -1853,17 +1876,25 @@ int wf_attn_forward_fp8_block(const void* q, int num_q_heads,
   Fp8Plan plan;
   rc = fp8_plan(sl, num_q_heads, Hk, splits, d->num_sms, &plan);
   if (rc) return rc;
-  wfk::AttnFewParams p;
+  alignas(64) wfk::AttnFewParams p;
   std::memset(&p, 0, sizeof(p));
+  // a box never crosses a page, nor a block (few rows) or a tile
+  p.box_rows = plan.few ? wfk::kFp8BlockTokens : gcd_int(ps, wfk::kBN);
+  const int64_t total_rows = static_cast<int64_t>(kv_pages->num_pages) * ps;
+  p.total_rows = static_cast<int>(total_rows);
+  if (!encode_codes(&p.tm_k, kv_pages->k_codes, D, Hk, total_rows, p.box_rows) ||
+      !encode_codes(&p.tm_v, kv_pages->v_codes, D, Hk, total_rows, p.box_rows))
+    return WF_ERR_CUDA;
   p.q = static_cast<const __nv_bfloat16*>(q);
-  p.k_codes = static_cast<const uint8_t*>(kv_pages->k_codes);
-  p.v_codes = static_cast<const uint8_t*>(kv_pages->v_codes);
   p.k_scale = static_cast<const uint8_t*>(kv_pages->k_scale);
   p.v_scale = static_cast<const uint8_t*>(kv_pages->v_scale);
   p.page_table = page_table_row;
   p.out = static_cast<__nv_bfloat16*>(out);
   p.lse = lse_or_null;
   p.status = d->status;
+  p.grid_abort = d->abort_word;
+  p.launch_id = g_launch_counter.fetch_add(1);
+  if (p.launch_id == 0) p.launch_id = g_launch_counter.fetch_add(1);
   p.T_q = sl.t_q;
   p.Hq = num_q_heads;
   p.Hk = Hk;
@@ -1888,13 +1919,19 @@ int wf_attn_forward_fp8_block(const void* q, int num_q_heads,
                                           align256(rows * D * sizeof(float)));
   }
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (!plan.few)
-    rc = D == 128 ? launch_fp8_blocks<128>(p, kv_pages, sl, plan, d, s)
-                  : launch_fp8_blocks<64>(p, kv_pages, sl, plan, d, s);
-  else if (D == 128)
-    rc = plan.mt == 1 ? launch_few<128, 1>(p, s) : launch_few<128, 2>(p, s);
-  else
-    rc = plan.mt == 1 ? launch_few<64, 1>(p, s) : launch_few<64, 2>(p, s);
+  if (plan.few) {
+    if (D == 128)
+      rc = plan.nt == 1   ? launch_few<128, 1>(p, s)
+           : plan.nt == 2 ? launch_few<128, 2>(p, s)
+                          : launch_few<128, 4>(p, s);
+    else
+      rc = plan.nt == 1   ? launch_few<64, 1>(p, s)
+           : plan.nt == 2 ? launch_few<64, 2>(p, s)
+                          : launch_few<64, 4>(p, s);
+    if (rc || plan.splits == 1) return rc;
+    return D == 128 ? launch_join<128>(p, s) : launch_join<64>(p, s);
+  }
+  rc = D == 128 ? launch_fp8_blocks<128>(p, sl, plan, s) : launch_fp8_blocks<64>(p, sl, plan, s);
   if (rc || plan.splits == 1) return rc;
   const int64_t threads = static_cast<int64_t>(sl.t_q) * num_q_heads * 32;
   const unsigned blocks =
