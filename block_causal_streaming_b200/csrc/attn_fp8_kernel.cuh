@@ -237,7 +237,8 @@ __global__ void __launch_bounds__(kFp8AttnThreads, 1)
             const uint4 v = x[2 * c + (i >> 1)];
             const uint32_t w0 = (i & 1) ? v.z : v.x, w1 = (i & 1) ? v.w : v.y;
             float y[4];
-            unpack4(make_uint2(w0, w1), y);
+            unpack2(w0, y);
+            unpack2(w1, y + 2);
             float back[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) y[k] *= f;

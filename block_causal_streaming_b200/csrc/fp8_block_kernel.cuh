@@ -16,8 +16,9 @@
 // the wavefront -- are kept: decoded, counted for the new scale and coded again.  Rows past the end
 // are dead, hold anything, and are left as they were.
 //
-// One warp per (block, head, tensor): the 16 rows sit in registers as fp32 (D/8 lanes per row,
-// as in the bf16 pass), so the block is read once and its scale is one warp reduction away.
+// One warp per (block, head, tensor): the 16 rows sit in registers as fp32 (D/16 lanes per row, as
+// in the bf16 pass), so the block is read once and its scale is one warp reduction away.  A CTA
+// takes one block's heads; the 16 tokens' cos and sin wait in shared memory for all of them.
 #pragma once
 
 #include <cuda_fp8.h>
@@ -37,6 +38,7 @@ struct Fp8BlockAppendParams {
   int weight_per_head;
   int token0, tokens, live;   // appended: [token0, token0 + tokens); live: [0, live)
   int H, page_size, num_pages;
+  int items;                  // (head, tensor) rows per CTA
   const int* pt_row;
   int* status;
 };
@@ -70,113 +72,138 @@ __device__ __forceinline__ float exp2_int(int e) {     // 2^e, e in [-126, 127]
   return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
 
+// grid: (blocks of 16 tokens, runs of p.items (head, tensor) rows; K rows first).
 template <int D, int kMode>
-__global__ void __launch_bounds__(kNormRopeThreads)
+__global__ void __launch_bounds__(kNormRopeThreads, 2)
     wf_fp8_block_append_kernel(const __grid_constant__ Fp8BlockAppendParams p) {
-  constexpr int LPR = D / 8, RPS = 32 / LPR, STEPS = kFp8BlockTokens / RPS;
-  const int lane = threadIdx.x & 31;
+  constexpr int LPR = D / 16, RPS = 32 / LPR, STEPS = kFp8BlockTokens / RPS;
+  constexpr int MAXP = D / 2;                        // pairs
+  // cos, sin of the block's tokens, as float4 (two pairs); a row is padded by one float4 so that
+  // the rows of a warp step start on different banks
+  constexpr int CSP = MAXP / 2 + 1;
+  __shared__ float4 angles[kMode != kRopeNone ? kFp8BlockTokens * CSP : 1];
+  __shared__ float stage_all[kMode == kRopeSplitPartial ? kNormRopeThreads * 16 : 1];
+  float* const stage = stage_all + (kMode == kRopeSplitPartial ? (threadIdx.x >> 5) * 512 : 0);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = lane % LPR, rsub = lane / LPR;
-  const int b0 = p.token0 / kFp8BlockTokens;
-  const int nb = (p.token0 + p.tokens - 1) / kFp8BlockTokens - b0 + 1;
-  const int64_t items = static_cast<int64_t>(nb) * 2 * p.H;
-  const int64_t warps = static_cast<int64_t>(gridDim.x) * (kNormRopeThreads / 32);
-  for (int64_t it = static_cast<int64_t>(blockIdx.x) * (kNormRopeThreads / 32) +
-                    (threadIdx.x >> 5);
-       it < items; it += warps) {
-    // heads fastest: the warps of a block share the tokens' cos and sin in L1
-    const int blk = b0 + static_cast<int>(it / (2 * p.H));
-    const int hh = static_cast<int>(it % (2 * p.H));
-    const int which = hh >= p.H ? 1 : 0, h = hh - which * p.H;
-    const int tok0 = blk * kFp8BlockTokens;
-    const int pg = __ldg(p.pt_row + tok0 / p.page_size);
-    if (pg < 0 || pg >= p.num_pages) {
-      if (lane == 0) atomicCAS(p.status, 0, 5 /* WF_ERR_PAGE_OOB */);
-      continue;
+  const int blk = p.token0 / kFp8BlockTokens + static_cast<int>(blockIdx.x);
+  const int tok0 = blk * kFp8BlockTokens;
+  // rows of the block: new ones [n0, n1), others live below n_live
+  const int n0 = max(p.token0 - tok0, 0);
+  const int n1 = min(p.token0 + p.tokens - tok0, kFp8BlockTokens);
+  const int n_live = min(p.live - tok0, kFp8BlockTokens);
+  const bool keeps = n0 > 0 || n1 < n_live;          // live rows that stay
+  const int pg = __ldg(p.pt_row + tok0 / p.page_size);
+  if (pg < 0 || pg >= p.num_pages) {
+    if (threadIdx.x == 0) atomicCAS(p.status, 0, 5 /* WF_ERR_PAGE_OOB */);
+    return;
+  }
+  if (kMode != kRopeNone) {
+    // a block with a position off the table is left as it was: its codes and scale belong together
+    bool bad = false;
+    const int per_row = p.rule.pairs / 2;
+    for (int i = threadIdx.x; i < kFp8BlockTokens * per_row; i += kNormRopeThreads) {
+      const int r = i / per_row, j = i - r * per_row;
+      float4 cs = make_float4(1.f, 0.f, 1.f, 0.f);
+      if (r >= n0 && r < n1) {
+        int pos[3];
+        if (load_positions(p.rule, tok0 + r - p.token0, pos)) cs = load_pairs(p.rule, pos, 2 * j);
+        else bad = true;
+      }
+      angles[r * CSP + j] = cs;
     }
-    const int64_t prow = static_cast<int64_t>(pg) * p.page_size + tok0 % p.page_size;
-    uint8_t* const codes = p.codes[which] + (prow * p.H + h) * D + 4 * sub;
+    if (__syncthreads_or(bad)) {
+      if (threadIdx.x == 0) atomicCAS(p.status, 0, 9 /* WF_ERR_POSITION */);
+      return;
+    }
+  }
+  const int64_t prow = static_cast<int64_t>(pg) * p.page_size + tok0 % p.page_size;
+  const int64_t cstep = static_cast<int64_t>(p.H) * D;
+  const int hh0 = static_cast<int>(blockIdx.y) * p.items;
+  const int hh1 = min(hh0 + p.items, 2 * p.H);
+  for (int hh = hh0 + warp; hh < hh1; hh += kNormRopeThreads / 32) {
+    const int which = hh >= p.H ? 1 : 0, h = hh - which * p.H;
+    uint8_t* const codes = p.codes[which] + (prow * p.H + h) * D + 8 * sub;
     uint8_t* const scale = p.scale[which] + prow / kFp8BlockTokens * p.H + h;
     const RowSet& s = p.set[which];
-    const int64_t cstep = static_cast<int64_t>(p.H) * D;
-
-    float w[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = 1.f;
-    if (s.weight != nullptr) {
-      const __nv_bfloat16* wp = s.weight + (p.weight_per_head ? h * D : 0) + 4 * sub;
-      unpack4(__ldg(reinterpret_cast<const uint2*>(wp)), w);
-      unpack4(__ldg(reinterpret_cast<const uint2*>(wp + D / 2)), w + 4);
-    }
-    // rows of the block: new ones [n0, n1), others live below `live`
-    const int n0 = max(p.token0 - tok0, 0);
-    const int n1 = min(p.token0 + p.tokens - tok0, kFp8BlockTokens);
-    const int n_live = min(p.live - tok0, kFp8BlockTokens);
-    float old_scale = 0.f;
-    if (n0 > 0 || n1 < n_live) old_scale = __uint_as_float(static_cast<uint32_t>(*scale) << 23);
-
-    float x[STEPS][8];
-    bool skip = false;                       // a new row has a position off the table
-    if (kMode != kRopeNone && which == 1) {
-      for (int i = lane; i < (n1 - n0) * p.rule.num_axes; i += 32) {
-        const int at = __ldg(p.rule.positions +
-                             static_cast<int64_t>(tok0 + n0 - p.token0) * p.rule.num_axes + i);
-        skip |= at < 0 || at >= p.rule.table_rows;
-      }
-    }
+    uint4 lo[STEPS], hi[STEPS];
 #pragma unroll
     for (int i = 0; i < STEPS; ++i) {
       const int r = i * RPS + rsub;
-      const bool fresh = r >= n0 && r < n1;
-      uint2 lo = make_uint2(0, 0), hi = make_uint2(0, 0);
-      if (fresh) {
+      lo[i] = hi[i] = make_uint4(0, 0, 0, 0);
+      if (r >= n0 && r < n1) {
         const __nv_bfloat16* src = s.src + static_cast<int64_t>(tok0 + r - p.token0) * s.stride +
-                                   static_cast<int64_t>(h) * D + 4 * sub;
-        lo = *reinterpret_cast<const uint2*>(src);
-        hi = *reinterpret_cast<const uint2*>(src + D / 2);
+                                   static_cast<int64_t>(h) * D + 8 * sub;
+        lo[i] = *reinterpret_cast<const uint4*>(src);
+        hi[i] = *reinterpret_cast<const uint4*>(src + D / 2);
       }
-      unpack4(lo, x[i]);
-      unpack4(hi, x[i] + 4);
-      if (!fresh && r < n_live) {
-        decode4(*reinterpret_cast<const uint32_t*>(codes + r * cstep), old_scale, x[i]);
-        decode4(*reinterpret_cast<const uint32_t*>(codes + r * cstep + D / 2), old_scale,
-                x[i] + 4);
-      }
+    }
+    uint4 wl = make_uint4(kOnes, kOnes, kOnes, kOnes), wh = wl;
+    if (s.weight != nullptr) {
+      const __nv_bfloat16* wp = s.weight + (p.weight_per_head ? h * D : 0) + 8 * sub;
+      wl = __ldg(reinterpret_cast<const uint4*>(wp));
+      wh = __ldg(reinterpret_cast<const uint4*>(wp + D / 2));
+    }
+    float x[STEPS][16];
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) {
+      unpack8(lo[i], x[i]);
+      unpack8(hi[i], x[i] + 8);
     }
     if (which == 0 && (kMode != kRopeNone || p.rule.norm)) {
 #pragma unroll
       for (int i = 0; i < STEPS; ++i) {
-        const int r = i * RPS + rsub;
-        const bool fresh = r >= n0 && r < n1;
         LaneAngles<kMode> a;
-        if (fresh) {
-          skip |= !load_angles<D, kMode>(p.rule, tok0 + r - p.token0, sub, a);
-        } else {
+        const float4* row = angles + (i * RPS + rsub) * CSP;
 #pragma unroll
-          for (int j = 0; j < LaneAngles<kMode>::N; ++j) a.cs[j] = make_float2(1.f, 0.f);
+        for (int j = 0; j < LaneAngles<kMode>::N; ++j) {
+          const int pr = lane_pair<D, kMode>(sub, j, p.rule.pairs);
+          a.cs[j] = pr >= 0 ? row[pr / 2] : make_float4(1.f, 0.f, 1.f, 0.f);
         }
-        float y[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = x[i][j];
-        norm_rope_row<D, kMode>(y, p.rule, sub, w, a);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[i][j] = fresh ? y[j] : x[i][j];
+        // a row that is not new is zeros here; without a norm it stays zeros, and a norm's
+        // rsqrt(0 + eps) may be infinite: it is replaced, or not stored, below
+        norm_rope_row<D, kMode>(x[i], p.rule, sub, wl, wh, a, stage);
       }
     }
-    // a block with such a row is left as it was: its codes and scale belong together
-    if (kMode != kRopeNone && __any_sync(0xffffffffu, skip)) {
-      if (lane == 0) atomicCAS(p.status, 0, 9 /* WF_ERR_POSITION */);
-      continue;
+    if (n0 > 0 || n1 < kFp8BlockTokens) {            // a block at an end of the append
+      const float old_scale =
+          keeps ? __uint_as_float(static_cast<uint32_t>(*scale) << 23) : 0.f;
+#pragma unroll
+      for (int i = 0; i < STEPS; ++i) {
+        const int r = i * RPS + rsub;
+        if (r >= n0 && r < n1) continue;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) x[i][j] = 0.f;
+        if (r < n_live) {
+          const uint2 c0 = *reinterpret_cast<const uint2*>(codes + r * cstep);
+          const uint2 c1 = *reinterpret_cast<const uint2*>(codes + r * cstep + D / 2);
+          decode4(c0.x, old_scale, x[i]);
+          decode4(c0.y, old_scale, x[i] + 4);
+          decode4(c1.x, old_scale, x[i] + 8);
+          decode4(c1.y, old_scale, x[i] + 12);
+        }
+      }
     }
     float top = 0.f;
+    float2 odd = make_float2(0.f, 0.f);              // NaN once a value is not finite
 #pragma unroll
     for (int i = 0; i < STEPS; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float m = fabsf(x[i][j]);
-        const bool finite = m < INFINITY;              // false for NaN
-        if (!finite) x[i][j] = __uint_as_float(0x7FFFFFFFu);
-        top = fmaxf(top, finite ? m : 0.f);
+      for (int j = 0; j < 16; j += 2) {
+        top = max3(top, fabsf(x[i][j]), fabsf(x[i][j + 1]));
+        odd = __ffma2_rn(make_float2(x[i][j], x[i][j + 1]), make_float2(0.f, 0.f), odd);
       }
+    if (__any_sync(0xffffffffu, isnan(odd.x + odd.y))) {
+      top = 0.f;
+#pragma unroll
+      for (int i = 0; i < STEPS; ++i)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const float m = fabsf(x[i][j]);
+          if (m < INFINITY) top = fmaxf(top, m);
+          else x[i][j] = __uint_as_float(0x7FFFFFFFu);
+        }
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     const int e = scale_exponent(top);
@@ -185,11 +212,11 @@ __global__ void __launch_bounds__(kNormRopeThreads)
     for (int i = 0; i < STEPS; ++i) {
       const int r = i * RPS + rsub;
       if (r < n1 || r < n_live) {
-        float y[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = x[i][j] * inv;
-        *reinterpret_cast<uint32_t*>(codes + r * cstep) = encode4(y);
-        *reinterpret_cast<uint32_t*>(codes + r * cstep + D / 2) = encode4(y + 4);
+        for (int j = 0; j < 16; ++j) x[i][j] *= inv;
+        *reinterpret_cast<uint2*>(codes + r * cstep) = make_uint2(encode4(x[i]), encode4(x[i] + 4));
+        *reinterpret_cast<uint2*>(codes + r * cstep + D / 2) =
+            make_uint2(encode4(x[i] + 8), encode4(x[i] + 12));
       }
     }
     if (lane == 0) *scale = static_cast<uint8_t>(e + 127);

@@ -9,14 +9,17 @@
 // Everything between the bf16 load and the one rounding of the result is fp32.  cos and sin come
 // from the caller's table (fp32, [position][pair]), so far positions keep the caller's accuracy.
 //
-// Row layout.  D / 8 lanes share a row; lane `sub` holds channels [4 sub, 4 sub + 4) and
-// [D/2 + 4 sub, ... + 4).  Interleaved pairs and the halves of a full split rotation then both sit
-// inside one lane; only a partial split rotation (2 pairs < D) exchanges values between lanes.
+// Row layout.  D / 16 lanes share a row; lane `sub` holds channels [8 sub, 8 sub + 8) and
+// [D/2 + 8 sub, ... + 8), two 16-byte loads.  Interleaved pairs and the halves of a full split
+// rotation then both sit inside one lane; only a partial split rotation (2 pairs < D) exchanges
+// values between lanes, through shared memory.
 #pragma once
 
 #include <cuda_bf16.h>
 
 #include <cstdint>
+
+#include "sm100.cuh"
 
 namespace wfk {
 
@@ -26,7 +29,7 @@ constexpr int kNormRopeThreads = 256;
 enum RopeMode { kRopeNone = 0, kRopeInterleaved = 1, kRopeSplit = 2, kRopeSplitPartial = 3 };
 
 struct NormRope {
-  const float2* table;        // [table_rows][pairs] (cos, sin)
+  const float2* table;        // [table_rows][pairs] (cos, sin), 16-byte aligned, pairs % 4 == 0
   const int* positions;       // [tokens][num_axes]
   int table_rows, pairs, num_axes;
   int axis1, axis2;           // first pair of axis 1 and of axis 2 (`pairs` when there is none)
@@ -34,51 +37,59 @@ struct NormRope {
   float eps;
 };
 
-// cos and sin of the pairs a lane turns, for one token.  N: 4 pairs, or 8 in kRopeSplitPartial
-// (both groups of a lane may belong to different pairs).
+// cos and sin of the pairs a lane turns, two pairs to a float4: 8 pairs, or one for each of the 16
+// channels in kRopeSplitPartial (the halves of a lane may belong to different pairs).
 template <int kMode>
 struct LaneAngles {
-  static constexpr int N = kMode == kRopeSplitPartial ? 8 : 4;
-  float2 cs[N];
+  static constexpr int N = kMode == kRopeNone ? 0 : kMode == kRopeSplitPartial ? 8 : 4;
+  float4 cs[N > 0 ? N : 1];
 };
 
-// Pair of slot j of a lane (j < 4: the low group, j >= 4: the high group), -1: not turned.
+// First pair of slot j (two pairs) of a lane, -1 when these are not turned.  In kRopeSplitPartial a
+// slot is two neighbouring channels; pairs % 4 == 0 keeps both on one side of every border.
 template <int D, int kMode>
 __device__ __forceinline__ int lane_pair(int sub, int j, int pairs) {
   if (kMode == kRopeInterleaved) {
-    const int i = j < 2 ? 2 * sub + j : D / 4 + 2 * sub + (j - 2);   // j: pair slot 0..3
+    const int i = j < 2 ? 4 * sub + 2 * j : D / 4 + 4 * sub + 2 * (j - 2);
     return i < pairs ? i : -1;
   }
-  if (kMode == kRopeSplit) return 4 * sub + j;                       // j: pair slot 0..3
-  const int ch = (j < 4 ? 4 * sub + j : D / 2 + 4 * sub + (j - 4));  // channel
+  if (kMode == kRopeSplit) return 8 * sub + 2 * j;
+  const int ch = j < 4 ? 8 * sub + 2 * j : D / 2 + 8 * sub + 2 * (j - 4);
   return ch < pairs ? ch : ch < 2 * pairs ? ch - pairs : -1;
 }
 
-// False when a position of token t lies outside the table (the caller skips the token).
-template <int D, int kMode>
-__device__ __forceinline__ bool load_angles(const NormRope& r, int64_t t, int sub,
-                                            LaneAngles<kMode>& a) {
-  if (kMode == kRopeNone) return true;
-  int pos[3] = {0, 0, 0};
+// A token's position along each axis; false when one lies outside the table.
+__device__ __forceinline__ bool load_positions(const NormRope& r, int64_t t, int (&pos)[3]) {
   bool ok = true;
 #pragma unroll
   for (int i = 0; i < 3; ++i) {
+    pos[i] = 0;
     if (i < r.num_axes) {
       pos[i] = __ldg(r.positions + t * r.num_axes + i);
       ok = ok && pos[i] >= 0 && pos[i] < r.table_rows;
     }
   }
-  if (!ok) return false;
+  return ok;
+}
+
+// (cos, sin) of pairs i and i + 1 (i even) at a position inside the table.
+__device__ __forceinline__ float4 load_pairs(const NormRope& r, const int (&pos)[3], int i) {
+  const int a = i >= r.axis2 ? pos[2] : i >= r.axis1 ? pos[1] : pos[0];
+  const int b = i + 1 >= r.axis2 ? pos[2] : i + 1 >= r.axis1 ? pos[1] : pos[0];
+  const float2* at = r.table + static_cast<int64_t>(a) * r.pairs + i;
+  if (a == b) return __ldg(reinterpret_cast<const float4*>(at));
+  const float2 x = __ldg(at), y = __ldg(r.table + static_cast<int64_t>(b) * r.pairs + i + 1);
+  return make_float4(x.x, x.y, y.x, y.y);
+}
+
+template <int D, int kMode>
+__device__ __forceinline__ void load_angles(const NormRope& r, const int (&pos)[3], int sub,
+                                            LaneAngles<kMode>& a) {
 #pragma unroll
   for (int j = 0; j < LaneAngles<kMode>::N; ++j) {
     const int p = lane_pair<D, kMode>(sub, j, r.pairs);
-    a.cs[j] = make_float2(1.f, 0.f);
-    if (p >= 0) {
-      const int at = p >= r.axis2 ? pos[2] : p >= r.axis1 ? pos[1] : pos[0];
-      a.cs[j] = __ldg(r.table + static_cast<int64_t>(at) * r.pairs + p);
-    }
+    a.cs[j] = p >= 0 ? load_pairs(r, pos, p) : make_float4(1.f, 0.f, 1.f, 0.f);
   }
-  return true;
 }
 
 // Sum over the LPR adjacent lanes of a row (every lane of the warp takes part).
@@ -89,63 +100,92 @@ __device__ __forceinline__ float row_sum(float v) {
   return v;
 }
 
-__device__ __forceinline__ void unpack4(uint2 w, float* x) {
-  x[0] = __uint_as_float(w.x << 16);
-  x[1] = __uint_as_float(w.x & 0xFFFF0000u);
-  x[2] = __uint_as_float(w.y << 16);
-  x[3] = __uint_as_float(w.y & 0xFFFF0000u);
+__device__ __forceinline__ void unpack2(uint32_t w, float* x) {
+  x[0] = __uint_as_float(w << 16);
+  x[1] = __uint_as_float(w & 0xFFFF0000u);
+}
+__device__ __forceinline__ void unpack8(uint4 w, float* x) {
+  unpack2(w.x, x);
+  unpack2(w.y, x + 2);
+  unpack2(w.z, x + 4);
+  unpack2(w.w, x + 6);
+}
+__device__ __forceinline__ uint4 pack8(const float* x) {
+  return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                    pack_bf16x2(x[6], x[7]));
 }
 
-// Norm and rotation of one row held by D/8 lanes.  Every lane of the warp calls it.
+// Norm and rotation of one row held by D/16 lanes: x[0..7] the low channels, x[8..15] the high.
+// wl, wh: the row's weights, 8 bf16 each.  Every lane of the warp calls it; `stage` is the warp's
+// 32 x 16 floats of shared memory, used in kRopeSplitPartial.
 template <int D, int kMode>
-__device__ __forceinline__ void norm_rope_row(float (&x)[8], const NormRope& r, int sub,
-                                              const float (&w)[8], const LaneAngles<kMode>& a) {
-  constexpr int LPR = D / 8;
+__device__ __forceinline__ void norm_rope_row(float (&x)[16], const NormRope& r, int sub,
+                                              uint4 wl, uint4 wh, const LaneAngles<kMode>& a,
+                                              float* stage) {
+  constexpr int LPR = D / 16;
   if (r.norm) {
-    float ss = 0.f;
+    float s0 = 0.f, s1 = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-    const float inv = rsqrtf(row_sum<LPR>(ss) * (1.f / D) + r.eps);
+    for (int i = 0; i < 8; ++i) {
+      s0 = fmaf(x[i], x[i], s0);
+      s1 = fmaf(x[8 + i], x[8 + i], s1);
+    }
+    const float inv = rsqrtf(row_sum<LPR>(s0 + s1) * (1.f / D) + r.eps);
+    float w[8];
+    unpack8(wl, w);
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = x[i] * inv * w[i];
+    unpack8(wh, w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[8 + i] = x[8 + i] * inv * w[i];
   }
   if (kMode == kRopeInterleaved) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < 8; ++j) {
+      const float4 cs = a.cs[j / 2];
+      const float c = j & 1 ? cs.z : cs.x, s = j & 1 ? cs.w : cs.y;
       const float u = x[2 * j], v = x[2 * j + 1];
-      x[2 * j] = u * a.cs[j].x - v * a.cs[j].y;
-      x[2 * j + 1] = u * a.cs[j].y + v * a.cs[j].x;
+      x[2 * j] = u * c - v * s;
+      x[2 * j + 1] = u * s + v * c;
     }
   } else if (kMode == kRopeSplit) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float u = x[j], v = x[4 + j];
-      x[j] = u * a.cs[j].x - v * a.cs[j].y;
-      x[4 + j] = u * a.cs[j].y + v * a.cs[j].x;
+    for (int j = 0; j < 8; ++j) {
+      const float4 cs = a.cs[j / 2];
+      const float c = j & 1 ? cs.z : cs.x, s = j & 1 ? cs.w : cs.y;
+      const float u = x[j], v = x[8 + j];
+      x[j] = u * c - v * s;
+      x[8 + j] = u * s + v * c;
     }
   } else if (kMode == kRopeSplitPartial) {
-    // 4-channel groups: group g < G turns with group g + G (G = pairs / 4 < LPR).  The low slot
-    // of lane `sub` is group `sub`, the high slot group LPR + sub.
-    const int G = r.pairs / 4;
-    const int lane = threadIdx.x & 31, base = lane - sub;
-    const bool first = sub < G;                               // low slot leads a pair
-    const bool low2 = sub >= G && sub < 2 * G;                // low slot follows one
-    const bool high2 = LPR + sub < 2 * G;                     // high slot follows one
-    const int partner = first ? sub + G : sub - G;            // group the low slot turns with
-    const int src = base + ((first ? partner % LPR : low2 ? partner : sub));
-    const int src_high = base + (high2 ? LPR + sub - G : sub);
+    float* const row = stage + ((threadIdx.x & 31) / LPR) * D;
+    __syncwarp();
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float from_low = __shfl_sync(0xffffffffu, x[j], src);
-      const float from_high = __shfl_sync(0xffffffffu, x[4 + j], src);
-      const float for_high = __shfl_sync(0xffffffffu, x[j], src_high);
-      const float other = first && partner >= LPR ? from_high : from_low;
-      const float c = a.cs[j].x, s = a.cs[j].y;
-      const float c2 = a.cs[4 + j].x, s2 = a.cs[4 + j].y;
-      const float lo = x[j], hi = x[4 + j];
-      x[j] = first ? lo * c - other * s : low2 ? other * s + lo * c : lo;
-      x[4 + j] = high2 ? for_high * s2 + hi * c2 : hi;
-    }
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < 8; i += 4)
+        *reinterpret_cast<float4*>(row + h * (D / 2) + 8 * sub + i) =
+            make_float4(x[8 * h + i], x[8 * h + i + 1], x[8 * h + i + 2], x[8 * h + i + 3]);
+    __syncwarp();
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < 8; i += 4) {       // 4 channels: pairs % 4 == 0 keeps them together
+        const int ch = h * (D / 2) + 8 * sub + i;
+        if (ch < 2 * r.pairs) {
+          const bool lead = ch < r.pairs;
+          const float4 o = *reinterpret_cast<const float4*>(row + (lead ? ch + r.pairs
+                                                                        : ch - r.pairs));
+          const float other[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float4 cs = a.cs[4 * h + (i + k) / 2];
+            const float c = k & 1 ? cs.z : cs.x, s = k & 1 ? cs.w : cs.y;
+            float& v = x[8 * h + i + k];
+            v = lead ? v * c - other[k] * s : other[k] * s + v * c;
+          }
+        }
+      }
   }
 }
 
@@ -171,14 +211,23 @@ struct NormRopeParams {
   int token0, page_size, num_pages;
 };
 
-// One warp per (token, run of `chunk` heads); a warp step covers 32 / (D/8) heads, so the token's
+constexpr uint32_t kOnes = 0x3F803F80u;           // two bf16 ones
+constexpr int kNormRopeBatch = 3;                 // warp steps whose loads are in flight together
+
+// One warp per (token, run of `chunk` heads); a warp step covers 32 / (D/16) heads, so the token's
 // cos and sin are read once and kept in registers while the heads go by.  kAppend: rows go to
 // their page, and set 1 (values) is copied bit for bit.
+//
+// Bound by HBM: 4 D bytes for each row, and the table from L2.  On 23 400 tokens of 12 + 12 heads of
+// 128 (288 MB): see the launch's rule for `chunk`; with 8-byte loads, one step at a time, this took
+// 79 us (3.6 TB/s).
 template <int D, int kMode, bool kAppend>
 __global__ void __launch_bounds__(kNormRopeThreads)
     wf_norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
-  constexpr int LPR = D / 8, RPS = 32 / LPR;      // lanes per row, rows per warp step
+  constexpr int LPR = D / 16, RPS = 32 / LPR, B = kNormRopeBatch;   // lanes per row, rows per step
+  __shared__ float stage_all[kMode == kRopeSplitPartial ? kNormRopeThreads * 16 : 1];
   const int lane = threadIdx.x & 31;
+  float* const stage = stage_all + (kMode == kRopeSplitPartial ? (threadIdx.x >> 5) * 512 : 0);
   const int sub = lane % LPR, rsub = lane / LPR;
   const int rows = p.set[0].heads + p.set[1].heads;
   const int64_t items = static_cast<int64_t>(p.tokens) * p.items_per_token;
@@ -200,41 +249,53 @@ __global__ void __launch_bounds__(kNormRopeThreads)
       row = static_cast<int64_t>(pg) * p.page_size + tok % p.page_size;
     }
     LaneAngles<kMode> a;
-    if (!load_angles<D, kMode>(p.rule, t, sub, a)) {   // the same answer in every lane
-      if (lane == 0) atomicCAS(p.status, 0, 9 /* WF_ERR_POSITION */);
-      continue;
+    if (kMode != kRopeNone) {
+      int pos[3];
+      if (!load_positions(p.rule, t, pos)) {      // the same answer in every lane
+        if (lane == 0) atomicCAS(p.status, 0, 9 /* WF_ERR_POSITION */);
+        continue;
+      }
+      load_angles<D, kMode>(p.rule, pos, sub, a);
     }
-    for (int rb = r0; rb < r1; rb += RPS) {
-      const int r = rb + rsub;
-      const bool in = r < r1;
-      const bool second = in && r >= p.set[0].heads;
-      const RowSet& s = p.set[second ? 1 : 0];
-      const int h = second ? r - p.set[0].heads : r;
-      const __nv_bfloat16* src = s.src + t * s.stride + static_cast<int64_t>(h) * D + 4 * sub;
-      uint2 lo = make_uint2(0, 0), hi = make_uint2(0, 0);
-      if (in) {
-        lo = *reinterpret_cast<const uint2*>(src);
-        hi = *reinterpret_cast<const uint2*>(src + D / 2);
-      }
-      float x[8], w[8];
-      unpack4(lo, x);
-      unpack4(hi, x + 4);
+    for (int rb = r0; rb < r1; rb += B * RPS) {
+      uint4 lo[B], hi[B];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = 1.f;
-      if (in && s.weight != nullptr) {
-        const __nv_bfloat16* wp = s.weight + (p.weight_per_head ? h * D : 0) + 4 * sub;
-        unpack4(__ldg(reinterpret_cast<const uint2*>(wp)), w);
-        unpack4(__ldg(reinterpret_cast<const uint2*>(wp + D / 2)), w + 4);
+      for (int b = 0; b < B; ++b) {
+        const int r = rb + b * RPS + rsub;
+        lo[b] = hi[b] = make_uint4(0, 0, 0, 0);
+        if (r < r1) {
+          const bool second = r >= p.set[0].heads;
+          const RowSet& s = p.set[second ? 1 : 0];
+          const int h = second ? r - p.set[0].heads : r;
+          const __nv_bfloat16* src = s.src + t * s.stride + static_cast<int64_t>(h) * D + 8 * sub;
+          lo[b] = *reinterpret_cast<const uint4*>(src);
+          hi[b] = *reinterpret_cast<const uint4*>(src + D / 2);
+        }
       }
-      norm_rope_row<D, kMode>(x, p.rule, sub, w, a);
-      if (!in) continue;
-      if (!(kAppend && second)) {
-        lo = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
-        hi = make_uint2(pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+#pragma unroll
+      for (int b = 0; b < B; ++b) {
+        if (rb + b * RPS >= r1) break;            // the whole warp
+        const int r = rb + b * RPS + rsub;
+        const bool in = r < r1;
+        const bool second = in && r >= p.set[0].heads;
+        const RowSet& s = p.set[second ? 1 : 0];
+        const int h = second ? r - p.set[0].heads : r;
+        uint4 wl = make_uint4(kOnes, kOnes, kOnes, kOnes), wh = wl;
+        if (in && s.weight != nullptr) {
+          const __nv_bfloat16* wp = s.weight + (p.weight_per_head ? h * D : 0) + 8 * sub;
+          wl = __ldg(reinterpret_cast<const uint4*>(wp));
+          wh = __ldg(reinterpret_cast<const uint4*>(wp + D / 2));
+        }
+        float x[16];
+        unpack8(lo[b], x);
+        unpack8(hi[b], x + 8);
+        norm_rope_row<D, kMode>(x, p.rule, sub, wl, wh, a, stage);
+        if (!in) continue;
+        __nv_bfloat16* dst = s.dst + (row * s.heads + h) * D + 8 * sub;
+        const bool copy = kAppend && second;
+        *reinterpret_cast<uint4*>(dst) = copy ? lo[b] : pack8(x);
+        *reinterpret_cast<uint4*>(dst + D / 2) = copy ? hi[b] : pack8(x + 8);
       }
-      __nv_bfloat16* dst = s.dst + (row * s.heads + h) * D + 4 * sub;
-      *reinterpret_cast<uint2*>(dst) = lo;
-      *reinterpret_cast<uint2*>(dst + D / 2) = hi;
     }
   }
 }

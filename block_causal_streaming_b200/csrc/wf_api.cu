@@ -1426,7 +1426,7 @@ int norm_rope_rule(const wf_norm_rope_t* rule, const int32_t* positions, int D,
   return WF_OK;
 }
 
-bool weight_ok(const void* w) { return (reinterpret_cast<uintptr_t>(w) & 7u) == 0; }
+bool weight_ok(const void* w) { return aligned16(w); }
 
 // A tensor of `tokens` rows of heads x D values, `stride` values apart (unused for one row).
 bool rows_ok(const void* p, int64_t stride, int heads, int D, int tokens) {
@@ -1445,7 +1445,7 @@ template <bool kAppend>
 int launch_norm_rope(wfk::NormRopeParams* p, wfk::RopeMode mode, int D, const DeviceState* d,
                      cudaStream_t s) {
   const int rows = p->set[0].heads + p->set[1].heads;
-  const int rps = 256 / D;                         // rows a warp covers in one step
+  const int rps = 512 / D;                         // rows a warp covers in one step
   const int steps = (rows + rps - 1) / rps;
   const int64_t want = static_cast<int64_t>(d->num_sms) * 48;      // warps that fill the GPU
   int per_token = static_cast<int>(std::min<int64_t>((want + p->tokens - 1) / p->tokens, steps));
@@ -1608,7 +1608,12 @@ int wf_kv_append_fp8_block(const wf_kv_pool_fp8_block_t* pool, int layer, int ch
   p.status = d->status;
   const int64_t nb = (p.token0 + int64_t{p.tokens} - 1) / wfk::kFp8BlockTokens -
                      p.token0 / wfk::kFp8BlockTokens + 1;
-  const int blocks = block_count(d, nb * 2 * p.H, 16);
+  // one CTA for all heads of a block when the blocks fill the GPU, else one for every 8 rows
+  const int warps = wfk::kNormRopeThreads / 32;
+  p.items = nb >= 2 * d->num_sms ? 2 * p.H : warps;
+  const int64_t runs = (2 * static_cast<int64_t>(p.H) + p.items - 1) / p.items;
+  if (nb > INT32_MAX || runs > 65535) return WF_ERR_SHAPE;
+  const dim3 blocks(static_cast<unsigned>(nb), static_cast<unsigned>(runs));
   const int th = wfk::kNormRopeThreads;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
 #define WF_LAUNCH(D_, M_) wfk::wf_fp8_block_append_kernel<D_, M_><<<blocks, th, 0, s>>>(p)

@@ -503,7 +503,7 @@ typedef struct {
  *                  aligned: contiguous tensors or slices of a fused projection's output.
  *   q_out, k_out   device bf16 [tokens][heads][D], contiguous, 16-byte aligned.  May be the input
  *                  itself where that is contiguous; no other overlap.
- *   q_weight, k_weight   device bf16 [D] or [heads][D], 8-byte aligned; NULL: ones.
+ *   q_weight, k_weight   device bf16 [D] or [heads][D], 16-byte aligned; NULL: ones.
  *   num_k_heads    0: queries only, k arguments unused.
  *   head_dim       64 or 128.
  *   positions      device int32 [tokens][num_axes] (unused without a rotation).
