@@ -174,6 +174,7 @@ __global__ void __launch_bounds__(kFp8AttnThreads, 1)
   const int kb = static_cast<int>(static_cast<int64_t>(split) * n_tiles / p.splits);
   const int nk = static_cast<int>(static_cast<int64_t>(split + 1) * n_tiles / p.splits) - kb;
 
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the join waits by itself
   const WaitCtx w{cta_abort, p.grid_abort, p.status, p.launch_id, 6 /* WF_ERR_TIMEOUT */,
                   kWaitTimeoutNs};
   if (threadIdx.x == 0) {
@@ -236,17 +237,11 @@ __global__ void __launch_bounds__(kFp8AttnThreads, 1)
           for (int i = 0; i < 4; ++i) {                     // 4 values: two words of bf16
             const uint4 v = x[2 * c + (i >> 1)];
             const uint32_t w0 = (i & 1) ? v.z : v.x, w1 = (i & 1) ? v.w : v.y;
-            float y[4];
-            unpack2(w0, y);
-            unpack2(w1, y + 2);
-            float back[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) y[k] *= f;
+            float4 y = make_float4(bf16_low(w0) * f, bf16_high(w0) * f, bf16_low(w1) * f,
+                                   bf16_high(w1) * f);
             hw[i] = encode4(y);
-            decode4(hw[i], 1.f, back);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) y[k] -= back[k];
-            lw[i] = encode4(y);
+            const float4 back = decode4(hw[i], 1.f);
+            lw[i] = encode4(make_float4(y.x - back.x, y.y - back.y, y.z - back.z, y.w - back.w));
           }
           st_shared_v4(hi_t + swz<D>(row, c), hw[0], hw[1], hw[2], hw[3]);
           st_shared_v4(lo_t + swz<D>(row, c), lw[0], lw[1], lw[2], lw[3]);

@@ -16,9 +16,12 @@
 // the wavefront -- are kept: decoded, counted for the new scale and coded again.  Rows past the end
 // are dead, hold anything, and are left as they were.
 //
-// One warp per (block, head, tensor): the 16 rows sit in registers as fp32 (D/16 lanes per row, as
-// in the bf16 pass), so the block is read once and its scale is one warp reduction away.  A CTA
-// takes one block's heads; the 16 tokens' cos and sin wait in shared memory for all of them.
+// Two warps per (block, head, tensor), 8 rows each: the rows sit in registers as fp32 (D/16 lanes per
+// row, as in the bf16 pass), so the block is read once; the scale is two warp reductions and a
+// barrier of the pair away.  A CTA takes one block's heads; the 16 tokens' cos and sin wait in shared
+// memory for all of them, and each head's values are asked for while the one before is worked on.
+// (One warp for all 16 rows holds 64 values a lane: 16 warps an SM, and 65 us against 43 on 23 400
+// tokens of 12 heads of 128.)
 #pragma once
 
 #include <cuda_fp8.h>
@@ -28,6 +31,8 @@
 namespace wfk {
 
 constexpr int kFp8BlockTokens = 16;
+constexpr int kFp8AppendPairs = kNormRopeThreads / 64;     // warp pairs of a CTA
+constexpr int kFp8AppendCtas = 2;                          // per SM, at least
 constexpr int kScaleExpMin = -100, kScaleExpMax = 119;
 
 struct Fp8BlockAppendParams {
@@ -44,21 +49,30 @@ struct Fp8BlockAppendParams {
 };
 
 // 4 e4m3 codes (code i in byte i) of 4 values already divided by the scale.
-__device__ __forceinline__ uint32_t encode4(const float* x) {
-  const uint32_t a = __nv_cvt_float2_to_fp8x2(make_float2(x[0], x[1]), __NV_SATFINITE, __NV_E4M3);
-  const uint32_t b = __nv_cvt_float2_to_fp8x2(make_float2(x[2], x[3]), __NV_SATFINITE, __NV_E4M3);
-  return (a & 0xFFFFu) | (b << 16);
+__device__ __forceinline__ uint32_t encode4(float4 x) {
+  uint32_t c;
+  asm("{\n\t.reg .b16 lo, hi;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
+      "mov.b32 %0, {lo, hi};\n\t}"
+      : "=r"(c)
+      : "f"(x.x), "f"(x.y), "f"(x.z), "f"(x.w));
+  return c;
 }
 
-__device__ __forceinline__ void decode4(uint32_t c, float scale, float* x) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const __half2 h(__nv_cvt_fp8x2_to_halfraw2(
-        static_cast<__nv_fp8x2_storage_t>((c >> (16 * i)) & 0xFFFFu), __NV_E4M3));
-    const float2 f = __half22float2(h);
-    x[2 * i] = f.x * scale;
-    x[2 * i + 1] = f.y * scale;
-  }
+// The largest of m >= 0, |a| and |b|; NaN when one of them is.
+__device__ __forceinline__ float max_abs(float m, float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(fabsf(a)), "f"(fabsf(b)));
+  return r;
+}
+
+__device__ __forceinline__ float4 decode4(uint32_t c, float scale) {
+  const float2 a = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(
+      static_cast<__nv_fp8x2_storage_t>(c & 0xFFFFu), __NV_E4M3)));
+  const float2 b = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(
+      static_cast<__nv_fp8x2_storage_t>(c >> 16), __NV_E4M3)));
+  return make_float4(a.x * scale, a.y * scale, b.x * scale, b.y * scale);
 }
 
 // Exponent of the smallest power of two that brings a >= 0 (finite) to 448 = 1.75 2^8 or less.
@@ -74,18 +88,21 @@ __device__ __forceinline__ float exp2_int(int e) {     // 2^e, e in [-126, 127]
 
 // grid: (blocks of 16 tokens, runs of p.items (head, tensor) rows; K rows first).
 template <int D, int kMode>
-__global__ void __launch_bounds__(kNormRopeThreads, 2)
+__global__ void __launch_bounds__(kNormRopeThreads, kFp8AppendCtas)
     wf_fp8_block_append_kernel(const __grid_constant__ Fp8BlockAppendParams p) {
-  constexpr int LPR = D / 16, RPS = 32 / LPR, STEPS = kFp8BlockTokens / RPS;
+  constexpr int LPR = D / 16, RPS = 32 / LPR, STEPS = kFp8BlockTokens / 2 / RPS;
   constexpr int MAXP = D / 2;                        // pairs
-  // cos, sin of the block's tokens, as float4 (two pairs); a row is padded by one float4 so that
+  // (cos, cos, sin, sin) of two pairs of the block's tokens; a row is padded by one float4 so that
   // the rows of a warp step start on different banks
   constexpr int CSP = MAXP / 2 + 1;
   __shared__ float4 angles[kMode != kRopeNone ? kFp8BlockTokens * CSP : 1];
   __shared__ float stage_all[kMode == kRopeSplitPartial ? kNormRopeThreads * 16 : 1];
-  float* const stage = stage_all + (kMode == kRopeSplitPartial ? (threadIdx.x >> 5) * 512 : 0);
+  __shared__ float tops[2][kFp8AppendPairs][2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int sub = lane % LPR, rsub = lane / LPR;
+  float* const stage = stage_all + (kMode == kRopeSplitPartial ? warp * 512 : 0);
+  const int sub = lane % LPR;
+  const int pair = warp >> 1, half = warp & 1;
+  const int r0 = half * 8 + lane / LPR;              // this lane's row of step i: r0 + i RPS
   const int blk = p.token0 / kFp8BlockTokens + static_cast<int>(blockIdx.x);
   const int tok0 = blk * kFp8BlockTokens;
   // rows of the block: new ones [n0, n1), others live below n_live
@@ -93,6 +110,28 @@ __global__ void __launch_bounds__(kNormRopeThreads, 2)
   const int n1 = min(p.token0 + p.tokens - tok0, kFp8BlockTokens);
   const int n_live = min(p.live - tok0, kFp8BlockTokens);
   const bool keeps = n0 > 0 || n1 < n_live;          // live rows that stay
+  const int hh0 = static_cast<int>(blockIdx.y) * p.items;
+  const int hh1 = min(hh0 + p.items, 2 * p.H);
+
+  uint4 lo[STEPS], hi[STEPS];
+  const bool whole = n1 - n0 == kFp8BlockTokens;
+  const auto load = [&](int hh) {
+    const int which = hh >= p.H ? 1 : 0, h = hh - which * p.H;
+    const RowSet& s = p.set[which];
+    const __nv_bfloat16* src =
+        s.src + static_cast<int64_t>(tok0 + r0 - p.token0) * s.stride + (h * D + 8 * sub);
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i, src += RPS * s.stride) {
+      const int r = r0 + i * RPS;
+      if (whole || (r >= n0 && r < n1)) {
+        lo[i] = *reinterpret_cast<const uint4*>(src);
+        hi[i] = *reinterpret_cast<const uint4*>(src + D / 2);
+      } else {
+        lo[i] = hi[i] = make_uint4(0, 0, 0, 0);
+      }
+    }
+  };
+  if (hh0 + pair < hh1) load(hh0 + pair);
   const int pg = __ldg(p.pt_row + tok0 / p.page_size);
   if (pg < 0 || pg >= p.num_pages) {
     if (threadIdx.x == 0) atomicCAS(p.status, 0, 5 /* WF_ERR_PAGE_OOB */);
@@ -101,10 +140,12 @@ __global__ void __launch_bounds__(kNormRopeThreads, 2)
   if (kMode != kRopeNone) {
     // a block with a position off the table is left as it was: its codes and scale belong together
     bool bad = false;
-    const int per_row = p.rule.pairs / 2;
+    // split partial: slots by pair; else by what the lanes turn, slots past the pairs stay as they are
+    constexpr int per_row = MAXP / 2;
     for (int i = threadIdx.x; i < kFp8BlockTokens * per_row; i += kNormRopeThreads) {
       const int r = i / per_row, j = i - r * per_row;
-      float4 cs = make_float4(1.f, 0.f, 1.f, 0.f);
+      float4 cs = make_float4(1.f, 1.f, 0.f, 0.f);
+      if (2 * j < p.rule.pairs)
       if (r >= n0 && r < n1) {
         int pos[3];
         if (load_positions(p.rule, tok0 + r - p.token0, pos)) cs = load_pairs(p.rule, pos, 2 * j);
@@ -118,108 +159,106 @@ __global__ void __launch_bounds__(kNormRopeThreads, 2)
     }
   }
   const int64_t prow = static_cast<int64_t>(pg) * p.page_size + tok0 % p.page_size;
-  const int64_t cstep = static_cast<int64_t>(p.H) * D;
-  const int hh0 = static_cast<int>(blockIdx.y) * p.items;
-  const int hh1 = min(hh0 + p.items, 2 * p.H);
-  for (int hh = hh0 + warp; hh < hh1; hh += kNormRopeThreads / 32) {
+  const int64_t cstep = static_cast<int64_t>(p.H) * D * RPS;       // from step to step
+  const int64_t code0 = (prow + r0) * p.H * D + 8 * sub;
+  const int64_t scale0 = prow / kFp8BlockTokens * p.H;
+  int turn = 0;
+#pragma unroll 1
+  for (int hh = hh0 + pair; hh < hh1; hh += kFp8AppendPairs, turn ^= 1) {
     const int which = hh >= p.H ? 1 : 0, h = hh - which * p.H;
-    uint8_t* const codes = p.codes[which] + (prow * p.H + h) * D + 8 * sub;
-    uint8_t* const scale = p.scale[which] + prow / kFp8BlockTokens * p.H + h;
-    const RowSet& s = p.set[which];
-    uint4 lo[STEPS], hi[STEPS];
+    uint8_t* const codes = p.codes[which] + code0 + h * D;
+    uint8_t* const scale = p.scale[which] + scale0 + h;
+    Row x[STEPS];
 #pragma unroll
-    for (int i = 0; i < STEPS; ++i) {
-      const int r = i * RPS + rsub;
-      lo[i] = hi[i] = make_uint4(0, 0, 0, 0);
-      if (r >= n0 && r < n1) {
-        const __nv_bfloat16* src = s.src + static_cast<int64_t>(tok0 + r - p.token0) * s.stride +
-                                   static_cast<int64_t>(h) * D + 8 * sub;
-        lo[i] = *reinterpret_cast<const uint4*>(src);
-        hi[i] = *reinterpret_cast<const uint4*>(src + D / 2);
-      }
-    }
-    uint4 wl = make_uint4(kOnes, kOnes, kOnes, kOnes), wh = wl;
-    if (s.weight != nullptr) {
-      const __nv_bfloat16* wp = s.weight + (p.weight_per_head ? h * D : 0) + 8 * sub;
-      wl = __ldg(reinterpret_cast<const uint4*>(wp));
-      wh = __ldg(reinterpret_cast<const uint4*>(wp + D / 2));
-    }
-    float x[STEPS][16];
-#pragma unroll
-    for (int i = 0; i < STEPS; ++i) {
-      unpack8(lo[i], x[i]);
-      unpack8(hi[i], x[i] + 8);
-    }
+    for (int i = 0; i < STEPS; ++i) unpack_row<kMode>(lo[i], hi[i], x[i]);
+    if (hh + kFp8AppendPairs < hh1) load(hh + kFp8AppendPairs);
     if (which == 0 && (kMode != kRopeNone || p.rule.norm)) {
+      Row w;
+      load_weight<D, kMode>(p.set[0].weight, p.weight_per_head ? static_cast<int64_t>(h) * D : 0,
+                            sub, w);
 #pragma unroll
       for (int i = 0; i < STEPS; ++i) {
-        LaneAngles<kMode> a;
-        const float4* row = angles + (i * RPS + rsub) * CSP;
-#pragma unroll
-        for (int j = 0; j < LaneAngles<kMode>::N; ++j) {
+        const float4* row = angles + (r0 + i * RPS) * CSP;
+        const auto at = [&](int j) {
+          if (kMode != kRopeSplitPartial) return row[lane_pair<D, kMode>(sub, j, MAXP) / 2];
           const int pr = lane_pair<D, kMode>(sub, j, p.rule.pairs);
-          a.cs[j] = pr >= 0 ? row[pr / 2] : make_float4(1.f, 0.f, 1.f, 0.f);
-        }
-        // a row that is not new is zeros here; without a norm it stays zeros, and a norm's
-        // rsqrt(0 + eps) may be infinite: it is replaced, or not stored, below
-        norm_rope_row<D, kMode>(x[i], p.rule, sub, wl, wh, a, stage);
+          return pr >= 0 ? row[pr / 2] : make_float4(1.f, 1.f, 0.f, 0.f);
+        };
+        // a row that is not new is zeros here, and a norm's rsqrt(0 + eps) may be infinite: the
+        // row is replaced below
+        norm_rope_row<D, kMode>(x[i], p.rule, sub, w, at, stage);
       }
     }
-    if (n0 > 0 || n1 < kFp8BlockTokens) {            // a block at an end of the append
+    if (!whole) {                                    // a block at an end of the append
       const float old_scale =
           keeps ? __uint_as_float(static_cast<uint32_t>(*scale) << 23) : 0.f;
 #pragma unroll
       for (int i = 0; i < STEPS; ++i) {
-        const int r = i * RPS + rsub;
+        const int r = r0 + i * RPS;
         if (r >= n0 && r < n1) continue;
-#pragma unroll
-        for (int j = 0; j < 16; ++j) x[i][j] = 0.f;
+        uint2 c0 = make_uint2(0, 0), c1 = c0;
         if (r < n_live) {
-          const uint2 c0 = *reinterpret_cast<const uint2*>(codes + r * cstep);
-          const uint2 c1 = *reinterpret_cast<const uint2*>(codes + r * cstep + D / 2);
-          decode4(c0.x, old_scale, x[i]);
-          decode4(c0.y, old_scale, x[i] + 4);
-          decode4(c1.x, old_scale, x[i] + 8);
-          decode4(c1.y, old_scale, x[i] + 12);
+          c0 = *reinterpret_cast<const uint2*>(codes + i * cstep);
+          c1 = *reinterpret_cast<const uint2*>(codes + i * cstep + D / 2);
         }
+        set_channels4<kMode>(x[i], 0, decode4(c0.x, old_scale));
+        set_channels4<kMode>(x[i], 1, decode4(c0.y, old_scale));
+        set_channels4<kMode>(x[i], 2, decode4(c1.x, old_scale));
+        set_channels4<kMode>(x[i], 3, decode4(c1.y, old_scale));
       }
     }
-    float top = 0.f;
-    float2 odd = make_float2(0.f, 0.f);              // NaN once a value is not finite
+    float top = 0.f;                                 // NaN or infinite when a value is
 #pragma unroll
     for (int i = 0; i < STEPS; ++i)
 #pragma unroll
-      for (int j = 0; j < 16; j += 2) {
-        top = max3(top, fabsf(x[i][j]), fabsf(x[i][j + 1]));
-        odd = __ffma2_rn(make_float2(x[i][j], x[i][j + 1]), make_float2(0.f, 0.f), odd);
+      for (int j = 0; j < 4; ++j) {
+        top = max_abs(top, x[i].u[j].x, x[i].u[j].y);
+        top = max_abs(top, x[i].v[j].x, x[i].v[j].y);
       }
-    if (__any_sync(0xffffffffu, isnan(odd.x + odd.y))) {
+    // magnitudes order as their bit patterns, infinity above all and NaN above that
+    uint32_t wtop = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
+    if (wtop >= 0x7F800000u) {
       top = 0.f;
+      auto clean = [&](float& v) {
+        const float m = fabsf(v);
+        if (m < INFINITY) top = fmaxf(top, m);
+        else v = __uint_as_float(0x7FFFFFFFu);
+      };
 #pragma unroll
       for (int i = 0; i < STEPS; ++i)
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const float m = fabsf(x[i][j]);
-          if (m < INFINITY) top = fmaxf(top, m);
-          else x[i][j] = __uint_as_float(0x7FFFFFFFu);
+        for (int j = 0; j < 4; ++j) {
+          clean(x[i].u[j].x);
+          clean(x[i].u[j].y);
+          clean(x[i].v[j].x);
+          clean(x[i].v[j].y);
         }
+      wtop = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (lane == 0) tops[turn][pair][half] = __uint_as_float(wtop);
+    // the pair's barrier; the other buffer is next turn's, so this one is not overwritten before the
+    // pair has met again
+    asm volatile("bar.sync %0, 64;" ::"r"(1 + pair) : "memory");
+    top = fmaxf(tops[turn][pair][0], tops[turn][pair][1]);
     const int e = scale_exponent(top);
     const float inv = exp2_int(-e);
+    const float2 inv2 = make_float2(inv, inv);
 #pragma unroll
     for (int i = 0; i < STEPS; ++i) {
-      const int r = i * RPS + rsub;
-      if (r < n1 || r < n_live) {
+      const int r = r0 + i * RPS;
+      if (whole || r < n1 || r < n_live) {
 #pragma unroll
-        for (int j = 0; j < 16; ++j) x[i][j] *= inv;
-        *reinterpret_cast<uint2*>(codes + r * cstep) = make_uint2(encode4(x[i]), encode4(x[i] + 4));
-        *reinterpret_cast<uint2*>(codes + r * cstep + D / 2) =
-            make_uint2(encode4(x[i] + 8), encode4(x[i] + 12));
+        for (int j = 0; j < 4; ++j) {
+          x[i].u[j] = __fmul2_rn(x[i].u[j], inv2);
+          x[i].v[j] = __fmul2_rn(x[i].v[j], inv2);
+        }
+        *reinterpret_cast<uint2*>(codes + i * cstep) =
+            make_uint2(encode4(channels4<kMode>(x[i], 0)), encode4(channels4<kMode>(x[i], 1)));
+        *reinterpret_cast<uint2*>(codes + i * cstep + D / 2) =
+            make_uint2(encode4(channels4<kMode>(x[i], 2)), encode4(channels4<kMode>(x[i], 3)));
       }
     }
-    if (lane == 0) *scale = static_cast<uint8_t>(e + 127);
+    if (half == 0 && lane == 0) *scale = static_cast<uint8_t>(e + 127);
   }
 }
 

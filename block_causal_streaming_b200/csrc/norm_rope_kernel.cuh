@@ -37,13 +37,23 @@ struct NormRope {
   float eps;
 };
 
-// cos and sin of the pairs a lane turns, two pairs to a float4: 8 pairs, or one for each of the 16
-// channels in kRopeSplitPartial (the halves of a lane may belong to different pairs).
+// A lane's 16 channels as eight packed pairs of floats, so that norm and rotation run two values to
+// an instruction.  Interleaved: u[i], v[i] are the first and second channels of pairs 2i and 2i + 1;
+// else u the low channels and v the high ones, in order (a full split rotation turns u with v).
+struct Row {
+  float2 u[4], v[4];
+};
+
+// cos and sin of what a lane turns, (cos, cos, sin, sin) of two pairs a slot: the pairs 2i and 2i + 1
+// of u[i], v[i], or in kRopeSplitPartial, where the channels of a lane may belong to different
+// pairs, those of its channels 2i and 2i + 1.
 template <int kMode>
 struct LaneAngles {
-  static constexpr int N = kMode == kRopeNone ? 0 : kMode == kRopeSplitPartial ? 8 : 4;
-  float4 cs[N > 0 ? N : 1];
+  float4 p[kMode == kRopeNone ? 1 : kMode == kRopeSplitPartial ? 8 : 4];
+  __device__ __forceinline__ float4 operator()(int j) const { return p[j]; }
 };
+template <int kMode>
+constexpr int kAngleSlots = kMode == kRopeNone ? 0 : kMode == kRopeSplitPartial ? 8 : 4;
 
 // First pair of slot j (two pairs) of a lane, -1 when these are not turned.  In kRopeSplitPartial a
 // slot is two neighbouring channels; pairs % 4 == 0 keeps both on one side of every border.
@@ -72,23 +82,26 @@ __device__ __forceinline__ bool load_positions(const NormRope& r, int64_t t, int
   return ok;
 }
 
-// (cos, sin) of pairs i and i + 1 (i even) at a position inside the table.
+// (cos, cos, sin, sin) of pairs i and i + 1 (i even) at a position inside the table.
 __device__ __forceinline__ float4 load_pairs(const NormRope& r, const int (&pos)[3], int i) {
   const int a = i >= r.axis2 ? pos[2] : i >= r.axis1 ? pos[1] : pos[0];
   const int b = i + 1 >= r.axis2 ? pos[2] : i + 1 >= r.axis1 ? pos[1] : pos[0];
   const float2* at = r.table + static_cast<int64_t>(a) * r.pairs + i;
-  if (a == b) return __ldg(reinterpret_cast<const float4*>(at));
+  if (a == b) {
+    const float4 x = __ldg(reinterpret_cast<const float4*>(at));
+    return make_float4(x.x, x.z, x.y, x.w);
+  }
   const float2 x = __ldg(at), y = __ldg(r.table + static_cast<int64_t>(b) * r.pairs + i + 1);
-  return make_float4(x.x, x.y, y.x, y.y);
+  return make_float4(x.x, y.x, x.y, y.y);
 }
 
 template <int D, int kMode>
 __device__ __forceinline__ void load_angles(const NormRope& r, const int (&pos)[3], int sub,
                                             LaneAngles<kMode>& a) {
 #pragma unroll
-  for (int j = 0; j < LaneAngles<kMode>::N; ++j) {
+  for (int j = 0; j < kAngleSlots<kMode>; ++j) {
     const int p = lane_pair<D, kMode>(sub, j, r.pairs);
-    a.cs[j] = p >= 0 ? load_pairs(r, pos, p) : make_float4(1.f, 0.f, 1.f, 0.f);
+    a.p[j] = p >= 0 ? load_pairs(r, pos, p) : make_float4(1.f, 1.f, 0.f, 0.f);
   }
 }
 
@@ -100,92 +113,110 @@ __device__ __forceinline__ float row_sum(float v) {
   return v;
 }
 
-__device__ __forceinline__ void unpack2(uint32_t w, float* x) {
-  x[0] = __uint_as_float(w << 16);
-  x[1] = __uint_as_float(w & 0xFFFF0000u);
-}
-__device__ __forceinline__ void unpack8(uint4 w, float* x) {
-  unpack2(w.x, x);
-  unpack2(w.y, x + 2);
-  unpack2(w.z, x + 4);
-  unpack2(w.w, x + 6);
-}
-__device__ __forceinline__ uint4 pack8(const float* x) {
-  return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                    pack_bf16x2(x[6], x[7]));
+__device__ __forceinline__ float bf16_low(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_high(uint32_t w) {
+  return __uint_as_float(w & 0xFFFF0000u);
 }
 
-// Norm and rotation of one row held by D/16 lanes: x[0..7] the low channels, x[8..15] the high.
-// wl, wh: the row's weights, 8 bf16 each.  Every lane of the warp calls it; `stage` is the warp's
-// 32 x 16 floats of shared memory, used in kRopeSplitPartial.
-template <int D, int kMode>
-__device__ __forceinline__ void norm_rope_row(float (&x)[16], const NormRope& r, int sub,
-                                              uint4 wl, uint4 wh, const LaneAngles<kMode>& a,
-                                              float* stage) {
+// 16 bf16 channels (low 8, high 8) <-> a lane's row.
+template <int kMode>
+__device__ __forceinline__ void unpack_row(uint4 lo, uint4 hi, Row& x) {
+  const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (kMode == kRopeInterleaved) {
+      x.u[i] = make_float2(bf16_low(w[2 * i]), bf16_low(w[2 * i + 1]));
+      x.v[i] = make_float2(bf16_high(w[2 * i]), bf16_high(w[2 * i + 1]));
+    } else {
+      x.u[i] = make_float2(bf16_low(w[i]), bf16_high(w[i]));
+      x.v[i] = make_float2(bf16_low(w[4 + i]), bf16_high(w[4 + i]));
+    }
+  }
+}
+// Channels 4 i .. 4 i + 3 of a lane's 16, in order (the high 8 from i = 2 on).
+template <int kMode>
+__device__ __forceinline__ float4 channels4(const Row& x, int i) {
+  if (kMode == kRopeInterleaved) return make_float4(x.u[i].x, x.v[i].x, x.u[i].y, x.v[i].y);
+  return i < 2 ? make_float4(x.u[2 * i].x, x.u[2 * i].y, x.u[2 * i + 1].x, x.u[2 * i + 1].y)
+               : make_float4(x.v[2 * i - 4].x, x.v[2 * i - 4].y, x.v[2 * i - 3].x,
+                             x.v[2 * i - 3].y);
+}
+template <int kMode>
+__device__ __forceinline__ void set_channels4(Row& x, int i, float4 c) {
+  if (kMode == kRopeInterleaved) {
+    x.u[i] = make_float2(c.x, c.z);
+    x.v[i] = make_float2(c.y, c.w);
+  } else if (i < 2) {
+    x.u[2 * i] = make_float2(c.x, c.y);
+    x.u[2 * i + 1] = make_float2(c.z, c.w);
+  } else {
+    x.v[2 * i - 4] = make_float2(c.x, c.y);
+    x.v[2 * i - 3] = make_float2(c.z, c.w);
+  }
+}
+template <int kMode>
+__device__ __forceinline__ uint4 pack_channels8(const Row& x, int half) {
+  const float4 a = channels4<kMode>(x, 2 * half), b = channels4<kMode>(x, 2 * half + 1);
+  return make_uint4(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w), pack_bf16x2(b.x, b.y),
+                    pack_bf16x2(b.z, b.w));
+}
+
+// Norm and rotation of one row held by D/16 lanes; w: the row's weights, angles(j): slot j's cos and
+// sin.  Every lane of the warp calls it; `stage` is the warp's 32 x 16 floats of shared memory, used in kRopeSplitPartial.
+template <int D, int kMode, typename Angles>
+__device__ __forceinline__ void norm_rope_row(Row& x, const NormRope& r, int sub, const Row& w,
+                                              const Angles& angles, float* stage) {
   constexpr int LPR = D / 16;
   if (r.norm) {
-    float s0 = 0.f, s1 = 0.f;
+    float2 s0 = make_float2(0.f, 0.f), s1 = s0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      s0 = fmaf(x[i], x[i], s0);
-      s1 = fmaf(x[8 + i], x[8 + i], s1);
+    for (int i = 0; i < 4; ++i) {
+      s0 = __ffma2_rn(x.u[i], x.u[i], s0);
+      s1 = __ffma2_rn(x.v[i], x.v[i], s1);
     }
-    const float inv = rsqrtf(row_sum<LPR>(s0 + s1) * (1.f / D) + r.eps);
-    float w[8];
-    unpack8(wl, w);
+    s0 = __fadd2_rn(s0, s1);
+    const float inv = rsqrtf(row_sum<LPR>(s0.x + s0.y) * (1.f / D) + r.eps);
+    const float2 inv2 = make_float2(inv, inv);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = x[i] * inv * w[i];
-    unpack8(wh, w);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[8 + i] = x[8 + i] * inv * w[i];
+    for (int i = 0; i < 4; ++i) {
+      x.u[i] = __fmul2_rn(__fmul2_rn(x.u[i], inv2), w.u[i]);
+      x.v[i] = __fmul2_rn(__fmul2_rn(x.v[i], inv2), w.v[i]);
+    }
   }
-  if (kMode == kRopeInterleaved) {
+  if constexpr (kMode == kRopeInterleaved || kMode == kRopeSplit) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float4 cs = a.cs[j / 2];
-      const float c = j & 1 ? cs.z : cs.x, s = j & 1 ? cs.w : cs.y;
-      const float u = x[2 * j], v = x[2 * j + 1];
-      x[2 * j] = u * c - v * s;
-      x[2 * j + 1] = u * s + v * c;
+    for (int i = 0; i < 4; ++i) {
+      const float4 p = angles(i);
+      const float2 c = make_float2(p.x, p.y), s = make_float2(p.z, p.w);
+      const float2 u = x.u[i], v = x.v[i];
+      x.u[i] = __ffma2_rn(v, make_float2(-p.z, -p.w), __fmul2_rn(u, c));
+      x.v[i] = __ffma2_rn(u, s, __fmul2_rn(v, c));
     }
-  } else if (kMode == kRopeSplit) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float4 cs = a.cs[j / 2];
-      const float c = j & 1 ? cs.z : cs.x, s = j & 1 ? cs.w : cs.y;
-      const float u = x[j], v = x[8 + j];
-      x[j] = u * c - v * s;
-      x[8 + j] = u * s + v * c;
-    }
-  } else if (kMode == kRopeSplitPartial) {
+  } else if constexpr (kMode == kRopeSplitPartial) {
     float* const row = stage + ((threadIdx.x & 31) / LPR) * D;
     __syncwarp();
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int i = 0; i < 8; i += 4)
-        *reinterpret_cast<float4*>(row + h * (D / 2) + 8 * sub + i) =
-            make_float4(x[8 * h + i], x[8 * h + i + 1], x[8 * h + i + 2], x[8 * h + i + 3]);
+    for (int i = 0; i < 4; ++i)
+      *reinterpret_cast<float4*>(row + (i / 2) * (D / 2) + 8 * sub + 4 * (i & 1)) =
+          channels4<kMode>(x, i);
     __syncwarp();
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int i = 0; i < 8; i += 4) {       // 4 channels: pairs % 4 == 0 keeps them together
-        const int ch = h * (D / 2) + 8 * sub + i;
-        if (ch < 2 * r.pairs) {
-          const bool lead = ch < r.pairs;
-          const float4 o = *reinterpret_cast<const float4*>(row + (lead ? ch + r.pairs
-                                                                        : ch - r.pairs));
-          const float other[4] = {o.x, o.y, o.z, o.w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float4 cs = a.cs[4 * h + (i + k) / 2];
-            const float c = k & 1 ? cs.z : cs.x, s = k & 1 ? cs.w : cs.y;
-            float& v = x[8 * h + i + k];
-            v = lead ? v * c - other[k] * s : other[k] * s + v * c;
-          }
-        }
+    for (int i = 0; i < 4; ++i) {            // 4 channels: pairs % 4 == 0 keeps them together
+      const int ch = (i / 2) * (D / 2) + 8 * sub + 4 * (i & 1);
+      if (ch < 2 * r.pairs) {
+        const bool lead = ch < r.pairs;
+        const float4 o = *reinterpret_cast<const float4*>(row + (lead ? ch + r.pairs
+                                                                      : ch - r.pairs));
+        const float4 p = angles(2 * i), q = angles(2 * i + 1);
+        float4 y = channels4<kMode>(x, i);
+        const float sgn = lead ? -1.f : 1.f;
+        y.x = y.x * p.x + sgn * (o.x * p.z);
+        y.y = y.y * p.y + sgn * (o.y * p.w);
+        y.z = y.z * q.x + sgn * (o.z * q.z);
+        y.w = y.w * q.y + sgn * (o.w * q.w);
+        set_channels4<kMode>(x, i, y);
       }
+    }
   }
 }
 
@@ -203,7 +234,7 @@ struct NormRopeParams {
   NormRope rule;
   int weight_per_head;
   int tokens;
-  int chunk;            // rows (heads of both sets together) per work item
+  int chunk;            // warp steps (of both sets together) per work item
   int items_per_token;
   int* status;
   // append only: token i of the call is logical token token0 + i
@@ -213,31 +244,64 @@ struct NormRopeParams {
 
 constexpr uint32_t kOnes = 0x3F803F80u;           // two bf16 ones
 constexpr int kNormRopeBatch = 3;                 // warp steps whose loads are in flight together
+constexpr int kNormRopeCtas = 3;                  // per SM, at least
 
-// One warp per (token, run of `chunk` heads); a warp step covers 32 / (D/16) heads, so the token's
-// cos and sin are read once and kept in registers while the heads go by.  kAppend: rows go to
-// their page, and set 1 (values) is copied bit for bit.
+// A lane's weights of one head (ones without a weight).
+template <int D, int kMode>
+__device__ __forceinline__ void load_weight(const __nv_bfloat16* weight, int64_t at, int sub,
+                                            Row& w) {
+  uint4 lo = make_uint4(kOnes, kOnes, kOnes, kOnes), hi = lo;
+  if (weight != nullptr) {
+    lo = __ldg(reinterpret_cast<const uint4*>(weight + at + 8 * sub));
+    hi = __ldg(reinterpret_cast<const uint4*>(weight + at + 8 * sub + D / 2));
+  }
+  unpack_row<kMode>(lo, hi, w);
+}
+
+// One warp per (token, run of `chunk` warp steps); a step covers 32 / (D/16) heads of one tensor,
+// the first tensor's steps before the second's, so the token's cos and sin and a tensor's weights
+// are read once and kept in registers while the heads go by.  kAppend: rows go to their page, and
+// set 1 (values) is copied bit for bit.
 //
-// Bound by HBM: 4 D bytes for each row, and the table from L2.  On 23 400 tokens of 12 + 12 heads of
-// 128 (288 MB): see the launch's rule for `chunk`; with 8-byte loads, one step at a time, this took
-// 79 us (3.6 TB/s).
+// Bound by HBM: 4 D bytes for each row, and the table from L2.
 template <int D, int kMode, bool kAppend>
-__global__ void __launch_bounds__(kNormRopeThreads)
+__global__ void __launch_bounds__(kNormRopeThreads, kNormRopeCtas)
     wf_norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
   constexpr int LPR = D / 16, RPS = 32 / LPR, B = kNormRopeBatch;   // lanes per row, rows per step
   __shared__ float stage_all[kMode == kRopeSplitPartial ? kNormRopeThreads * 16 : 1];
   const int lane = threadIdx.x & 31;
   float* const stage = stage_all + (kMode == kRopeSplitPartial ? (threadIdx.x >> 5) * 512 : 0);
   const int sub = lane % LPR, rsub = lane / LPR;
-  const int rows = p.set[0].heads + p.set[1].heads;
+  const int steps0 = (p.set[0].heads + RPS - 1) / RPS;
+  const int steps = steps0 + (p.set[1].heads + RPS - 1) / RPS;
   const int64_t items = static_cast<int64_t>(p.tokens) * p.items_per_token;
   const int64_t warps = static_cast<int64_t>(gridDim.x) * (kNormRopeThreads / 32);
   for (int64_t it = static_cast<int64_t>(blockIdx.x) * (kNormRopeThreads / 32) +
                     (threadIdx.x >> 5);
        it < items; it += warps) {
     const int64_t t = it / p.items_per_token;
-    const int r0 = static_cast<int>(it - t * p.items_per_token) * p.chunk;
-    const int r1 = min(r0 + p.chunk, rows);
+    const int st0 = static_cast<int>(it - t * p.items_per_token) * p.chunk;
+    const int st1 = min(st0 + p.chunk, steps);
+    // the first heads' values, the token's page and its positions are asked for together
+    uint4 lo[B], hi[B];
+    const auto load = [&](const RowSet& s, int hb, int h1) {
+      const __nv_bfloat16* const src = s.src + t * s.stride + 8 * sub;
+#pragma unroll
+      for (int b = 0; b < B; ++b) {
+        const int h = hb + b * RPS + rsub;
+        lo[b] = hi[b] = make_uint4(0, 0, 0, 0);
+        if (h < h1) {
+          lo[b] = *reinterpret_cast<const uint4*>(src + h * D);
+          hi[b] = *reinterpret_cast<const uint4*>(src + h * D + D / 2);
+        }
+      }
+    };
+    const int first = st0 < steps0 ? 0 : 1;
+    const auto begin = [&](int which) { return max(st0 - (which ? steps0 : 0), 0) * RPS; };
+    const auto end = [&](int which) {
+      return min((st1 - (which ? steps0 : 0)) * RPS, p.set[which].heads);
+    };
+    load(p.set[first], begin(first), end(first));
     int64_t row = t;                              // destination row of the token
     if (kAppend) {
       const int tok = p.token0 + static_cast<int>(t);
@@ -257,44 +321,35 @@ __global__ void __launch_bounds__(kNormRopeThreads)
       }
       load_angles<D, kMode>(p.rule, pos, sub, a);
     }
-    for (int rb = r0; rb < r1; rb += B * RPS) {
-      uint4 lo[B], hi[B];
+#pragma unroll 1
+    for (int which = first; which < 2; ++which) {
+      const RowSet& s = p.set[which];
+      const int h0 = begin(which), h1 = end(which);
+      if (h0 >= h1) continue;
+      __nv_bfloat16* const dst = s.dst + row * s.heads * D + 8 * sub;
+      const bool copy = kAppend && which == 1;
+      Row w;
+      if (!copy) load_weight<D, kMode>(s.weight, 0, sub, w);
+      for (int hb = h0; hb < h1; hb += B * RPS) {
+        if (which != first || hb != h0) load(s, hb, h1);
 #pragma unroll
-      for (int b = 0; b < B; ++b) {
-        const int r = rb + b * RPS + rsub;
-        lo[b] = hi[b] = make_uint4(0, 0, 0, 0);
-        if (r < r1) {
-          const bool second = r >= p.set[0].heads;
-          const RowSet& s = p.set[second ? 1 : 0];
-          const int h = second ? r - p.set[0].heads : r;
-          const __nv_bfloat16* src = s.src + t * s.stride + static_cast<int64_t>(h) * D + 8 * sub;
-          lo[b] = *reinterpret_cast<const uint4*>(src);
-          hi[b] = *reinterpret_cast<const uint4*>(src + D / 2);
+        for (int b = 0; b < B; ++b) {
+          if (hb + b * RPS >= h1) break;          // the whole warp
+          const int h = hb + b * RPS + rsub;
+          if (!copy) {
+            if (p.weight_per_head && h < h1)
+              load_weight<D, kMode>(s.weight, static_cast<int64_t>(h) * D, sub, w);
+            Row x;
+            unpack_row<kMode>(lo[b], hi[b], x);
+            norm_rope_row<D, kMode>(x, p.rule, sub, w, a, stage);
+            lo[b] = pack_channels8<kMode>(x, 0);
+            hi[b] = pack_channels8<kMode>(x, 1);
+          }
+          if (h < h1) {
+            *reinterpret_cast<uint4*>(dst + h * D) = lo[b];
+            *reinterpret_cast<uint4*>(dst + h * D + D / 2) = hi[b];
+          }
         }
-      }
-#pragma unroll
-      for (int b = 0; b < B; ++b) {
-        if (rb + b * RPS >= r1) break;            // the whole warp
-        const int r = rb + b * RPS + rsub;
-        const bool in = r < r1;
-        const bool second = in && r >= p.set[0].heads;
-        const RowSet& s = p.set[second ? 1 : 0];
-        const int h = second ? r - p.set[0].heads : r;
-        uint4 wl = make_uint4(kOnes, kOnes, kOnes, kOnes), wh = wl;
-        if (in && s.weight != nullptr) {
-          const __nv_bfloat16* wp = s.weight + (p.weight_per_head ? h * D : 0) + 8 * sub;
-          wl = __ldg(reinterpret_cast<const uint4*>(wp));
-          wh = __ldg(reinterpret_cast<const uint4*>(wp + D / 2));
-        }
-        float x[16];
-        unpack8(lo[b], x);
-        unpack8(hi[b], x + 8);
-        norm_rope_row<D, kMode>(x, p.rule, sub, wl, wh, a, stage);
-        if (!in) continue;
-        __nv_bfloat16* dst = s.dst + (row * s.heads + h) * D + 8 * sub;
-        const bool copy = kAppend && second;
-        *reinterpret_cast<uint4*>(dst) = copy ? lo[b] : pack8(x);
-        *reinterpret_cast<uint4*>(dst + D / 2) = copy ? hi[b] : pack8(x + 8);
       }
     }
   }

@@ -1444,13 +1444,13 @@ int block_count(const DeviceState* d, int64_t items, int per_sm) {
 template <bool kAppend>
 int launch_norm_rope(wfk::NormRopeParams* p, wfk::RopeMode mode, int D, const DeviceState* d,
                      cudaStream_t s) {
-  const int rows = p->set[0].heads + p->set[1].heads;
   const int rps = 512 / D;                         // rows a warp covers in one step
-  const int steps = (rows + rps - 1) / rps;
+  const int steps = (p->set[0].heads + rps - 1) / rps + (p->set[1].heads + rps - 1) / rps;
   const int64_t want = static_cast<int64_t>(d->num_sms) * 48;      // warps that fill the GPU
-  int per_token = static_cast<int>(std::min<int64_t>((want + p->tokens - 1) / p->tokens, steps));
-  p->chunk = (steps + per_token - 1) / per_token * rps;
-  p->items_per_token = (rows + p->chunk - 1) / p->chunk;
+  const int per_token = static_cast<int>(std::min<int64_t>((want + p->tokens - 1) / p->tokens,
+                                                           steps));
+  p->chunk = (steps + per_token - 1) / per_token;
+  p->items_per_token = (steps + p->chunk - 1) / p->chunk;
   const int blocks = block_count(d, static_cast<int64_t>(p->tokens) * p->items_per_token, 16);
   const int th = wfk::kNormRopeThreads;
 #define WF_LAUNCH(D_, M_) wfk::wf_norm_rope_kernel<D_, M_, kAppend><<<blocks, th, 0, s>>>(*p)
@@ -1608,9 +1608,8 @@ int wf_kv_append_fp8_block(const wf_kv_pool_fp8_block_t* pool, int layer, int ch
   p.status = d->status;
   const int64_t nb = (p.token0 + int64_t{p.tokens} - 1) / wfk::kFp8BlockTokens -
                      p.token0 / wfk::kFp8BlockTokens + 1;
-  // one CTA for all heads of a block when the blocks fill the GPU, else one for every 8 rows
-  const int warps = wfk::kNormRopeThreads / 32;
-  p.items = nb >= 2 * d->num_sms ? 2 * p.H : warps;
+  // one CTA for all heads of a block when the blocks fill the GPU, else one for a head a warp pair
+  p.items = nb >= 2 * d->num_sms ? 2 * p.H : wfk::kFp8AppendPairs;
   const int64_t runs = (2 * static_cast<int64_t>(p.H) + p.items - 1) / p.items;
   if (nb > INT32_MAX || runs > 65535) return WF_ERR_SHAPE;
   const dim3 blocks(static_cast<unsigned>(nb), static_cast<unsigned>(runs));
@@ -1678,18 +1677,23 @@ struct Fp8Plan {
 };
 
 constexpr int kFewRows = 32;        // packed rows up to which the few-row kernel runs
+constexpr int kMaxRowBlockSplits = 64;
 
 // Key parts of each row block: the count a model of the grid finds shortest, in times of a key
 // tile.  Blocks go out most keys first, one to an SM at a time; each costs its tiles and about 2.5
 // for its start and end; the join of a split costs about kMergePerPart for a million parts of rows.
+// Blocks that see no key come last and cost next to nothing.
 int fp8_row_block_splits(const SegmentList& sl, const Fp8Plan& plan, int Hq, int Hk,
                          int num_sms) {
-  const int64_t units = static_cast<int64_t>(plan.tiles) * Hk;
+  int seen = 0;                                            // row blocks that see a key
+  for (int i = 0; i < sl.n; ++i)
+    if (sl.kv[plan.order[i]] > 0) seen = plan.tile_end[i];
+  const int64_t units = static_cast<int64_t>(seen) * Hk;
   if (units >= 2 * static_cast<int64_t>(num_sms)) return 1;
   int best = 1;
   double best_cost = 0;
-  const int most = (sl.max_kv + wfk::kBN - 1) / wfk::kBN;
-  for (int S = 1; S <= std::min(kMaxSplits, std::max(most, 1)); ++S) {
+  const int most = std::max((sl.max_kv + wfk::kBN - 1) / wfk::kBN, 1);
+  for (int S = 1; S <= std::min(kMaxRowBlockSplits, most); ++S) {
     double cost = S > 1 ? kMergePerPart * sl.t_q * Hq * S / 1e6 : 0;
     int seg = 0;
     for (int64_t u = 0; u < units * S; u += num_sms) {     // one wave after the other
@@ -1753,7 +1757,12 @@ int launch_few(const wfk::AttnFewParams& p, cudaStream_t s) {
   return cudaGetLastError() == cudaSuccess ? WF_OK : WF_ERR_CUDA;
 }
 
-// The join of the few-row kernel's parts, its blocks launched while that kernel still runs.
+// (row, head) pairs up to which a block each joins the parts; above, a warp each (the merge kernel).
+// Measured, join / merge, keys 37 440 x 12 heads: 1536 pairs 61 / 64 us the call, 6144 pairs
+// 135 / 128; keys 8192 x 8 heads: 384 pairs 18.1 / 21.8, 2048 pairs 33.6 / 32.4.
+constexpr int kJoinRows = 2048;
+
+// The join of a launch's parts, its blocks launched while that one still runs.
 template <int D>
 int launch_join(const wfk::AttnFewParams& p, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
@@ -1938,6 +1947,8 @@ int wf_attn_forward_fp8_block(const void* q, int num_q_heads,
   }
   rc = D == 128 ? launch_fp8_blocks<128>(p, sl, plan, s) : launch_fp8_blocks<64>(p, sl, plan, s);
   if (rc || plan.splits == 1) return rc;
+  if (static_cast<int64_t>(sl.t_q) * num_q_heads <= kJoinRows)
+    return D == 128 ? launch_join<128>(p, s) : launch_join<64>(p, s);
   const int64_t threads = static_cast<int64_t>(sl.t_q) * num_q_heads * 32;
   const unsigned blocks =
       static_cast<unsigned>((threads + wfk::kCombineThreads - 1) / wfk::kCombineThreads);
