@@ -46,5 +46,6 @@ __all__ = list(_ABI_NAMES)
 def __getattr__(name):
     if name in _ABI_NAMES:
         from . import _abi
-        return getattr(_abi, name)
+        value = globals()[name] = getattr(_abi, name)     # found directly from now on
+        return value
     raise AttributeError(name)

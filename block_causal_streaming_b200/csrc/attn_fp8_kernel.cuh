@@ -27,8 +27,17 @@
 // tiles past the limit are not read, the last tile's columns past it get weight 0 and its values
 // are zeroed.
 //
+// One CTA an SM works through a list of pieces, a piece being a unit or a run of its key tiles: whole
+// units first, unit k G + i to CTA i, then an even share of the tiles of the units that are left, cut
+// wherever the share ends.  Pieces of a cut unit go to a workspace and are joined by a second
+// launch.  So the SMs end together whatever the number of units (228 units of equal length on 148
+// SMs: 1.54 units each, where whole units take 2 turns and uniform parts 4 to 5 percent of joining
+// and 10 of idle SMs), and loads run ahead from one piece into the next.
+//
 // Warp roles (512 threads): 0-3, 4-7 softmax of Q tile 0, 1 (thread = row; they also split Q);
-// 8 TMA of K, key scales; 9 issues QK^T; 10 issues P.V; 11 TMA of V codes; 12-15 convert V.
+// 8 TMA of K, key scales; 9 issues QK^T; 10 issues P.V; 11 TMA of V codes; 12-15 convert V.  Rings
+// and barrier phases run on over the pieces: `it` counts key tiles, and what belongs to one Q tile is
+// counted for it alone, since a unit's last 128 rows may be missing.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -52,6 +61,35 @@ static_assert(256 * kFp8RegSoftmax + 256 * kFp8RegOther <= 512 * kFp8LaunchRegs,
 
 constexpr float kTrail = 2.f, kShift = 15.f - kTrail;   // weights: at most 2^15
 
+constexpr int kFp8MaxCtas = 160;             // CTAs of a launch (one an SM)
+constexpr int kUnitTileRows = 2 * kBM;       // packed rows of a unit
+
+// The units of a launch: row blocks of the segments (most keys first), heads in groups; those that
+// see no key come last and apart.
+struct Fp8Units {
+  int Hk, group, head_group;                 // head_group: K/V heads per dispatch group
+  int pairs;                                 // row blocks that see keys
+  int seg_pair_end[kFewSegs];                // row blocks up to and including segment i
+  int seg_row0[kFewSegs];
+  int seg_rows[kFewSegs];
+  int seg_kv[kFewSegs];
+};
+
+struct UnitAt {
+  int seg, m0, head;
+};
+__host__ __device__ __forceinline__ UnitAt unit_at(const Fp8Units& u, int unit) {
+  const int per_group = u.pairs * u.head_group;
+  const int hgrp = unit / per_group, in_group = unit - hgrp * per_group;
+  const int block = in_group / u.head_group;
+  UnitAt r;
+  r.head = hgrp * u.head_group + in_group % u.head_group;
+  r.seg = 0;
+  while (block >= u.seg_pair_end[r.seg]) ++r.seg;
+  r.m0 = (block - (r.seg > 0 ? u.seg_pair_end[r.seg - 1] : 0)) * kUnitTileRows;
+  return r;
+}
+
 struct AttnFp8Params {
   CUtensorMap tm_k;  // e4m3 (D, Hk, num_pages * page_size), box (D, 1, box_rows), D-byte swizzle
   CUtensorMap tm_v;
@@ -61,20 +99,85 @@ struct AttnFp8Params {
   const int* page_table;
   __nv_bfloat16* out;
   float* lse;
-  float* part_o;
-  float* part_lse;
+  float* part_o;                     // [slots][256 packed rows][D], a slot for each part of a cut unit
+  float* part_lse;                   // [slots][256]
   int* status;
   unsigned* grid_abort;
   unsigned launch_id;
-  int T_q, Hq, Hk, group, page_size, num_pages, total_rows, box_rows, splits;
-  int head_group;                    // K/V heads per dispatch group (divides Hk)
-  int pairs;                         // row blocks of all segments
+  int T_q, Hq, Hk, page_size, num_pages, total_rows, box_rows;
   float sl2;                         // scale * log2(e)
-  // segments in dispatch order (most keys first)
-  int seg_pair_end[kFewSegs];        // row blocks up to and including segment i
-  int seg_row0[kFewSegs];
-  int seg_rows[kFewSegs];
-  int seg_kv[kFewSegs];
+  Fp8Units units;
+  int n_units, n_whole;              // units that see keys; the first n_whole go out whole
+  int n_blank;                       // units that see none
+  // share of CTA i in the tiles of units n_whole ..: from tile share_tile[i] of unit share_unit[i],
+  // share_tiles[i] of them; its parts of units go to the slots from share_slot[i] on
+  int share_unit[kFp8MaxCtas];
+  int share_tile[kFp8MaxCtas];
+  int share_tiles[kFp8MaxCtas];
+  int share_slot[kFp8MaxCtas];
+};
+static_assert(sizeof(AttnFp8Params) <= 4096, "kernel parameters");
+
+// A piece of work, the same in every warp of the CTA.
+struct Piece {
+  int seg, m0, head, nq;             // nq: Q tiles with rows
+  int n_max, kb, nk;                 // keys the rows see; tiles [kb, kb + nk) of them
+  int m_total;                       // packed rows of the segment
+  int slot;                          // workspace slot of a part, -1: whole
+};
+struct PieceList {
+  int unit, share_unit, share_tile, share_left, slot, blank;
+  __device__ __forceinline__ explicit PieceList(const AttnFp8Params& p) {
+    const int i = static_cast<int>(blockIdx.x);
+    unit = i;
+    share_unit = p.share_unit[i];
+    share_tile = p.share_tile[i];
+    share_left = p.share_tiles[i];
+    slot = p.share_slot[i];
+    blank = i;
+  }
+  __device__ __forceinline__ bool next(const AttnFp8Params& p, Piece* w) {
+    const Fp8Units& u = p.units;
+    int at = unit, first = 0, len = -1;                // len < 0: to the end
+    w->slot = -1;
+    if (unit < p.n_whole) {
+      unit += static_cast<int>(gridDim.x);
+    } else if (share_left > 0) {
+      at = share_unit++;
+      first = share_tile;
+      len = share_left;
+      share_tile = 0;
+    } else if (blank < p.n_blank) {
+      const int block = u.pairs + blank / p.Hk;        // segments that see nothing: the last ones
+      w->head = blank % p.Hk;
+      blank += static_cast<int>(gridDim.x);
+      int seg = 0;
+      while (block >= u.seg_pair_end[seg]) ++seg;
+      w->seg = seg;
+      w->m0 = (block - (seg > 0 ? u.seg_pair_end[seg - 1] : 0)) * kUnitTileRows;
+      w->m_total = u.seg_rows[seg] * u.group;
+      w->nq = w->m0 + kBM < w->m_total ? 2 : 1;
+      w->n_max = w->kb = w->nk = 0;
+      return true;
+    } else {
+      return false;
+    }
+    const UnitAt r = unit_at(u, at);
+    w->seg = r.seg;
+    w->m0 = r.m0;
+    w->head = r.head;
+    w->m_total = u.seg_rows[r.seg] * u.group;
+    w->nq = r.m0 + kBM < w->m_total ? 2 : 1;
+    w->n_max = u.seg_kv[r.seg];
+    const int tiles = (w->n_max + kBN - 1) / kBN;
+    w->kb = first;
+    w->nk = len < 0 ? tiles : min(tiles - first, len);
+    if (len >= 0) {
+      share_left -= w->nk;
+      if (w->nk < tiles) w->slot = slot++;
+    }
+    return true;
+  }
 };
 
 template <int D>
@@ -94,12 +197,17 @@ struct AttnFp8Smem {
   static constexpr uint32_t V_OFF = C_OFF + NC * CTILE;
   static constexpr uint32_t KS_OFF = V_OFF + NV * VTILE;  // key scales [2 NK][8] floats
   static constexpr uint32_t BAR_OFF = KS_OFF + 2 * NK * 32;
-  static constexpr int B_Q = 0, B_KF = 1, B_KE = B_KF + NK, B_CF = B_KE + NK, B_CE = B_CF + NC,
+  static constexpr int B_Q = 0, B_KF = 2, B_KE = B_KF + NK, B_CF = B_KE + NK, B_CE = B_CF + NC,
                        B_VF = B_CE + NC, B_VE = B_VF + NV, B_S = B_VE + NV, B_P = B_S + 2,
-                       B_O = B_P + 2, B_SF = B_O + 2, B_EM = B_SF + 1, B_DRAIN = B_EM + 1,
-                       NBAR = B_DRAIN + 2;
-  static constexpr uint32_t MISC_OFF = BAR_OFF + NBAR * 8;
-  static constexpr uint32_t BYTES = MISC_OFF + 32;
+                       B_O = B_P + 2, B_SF = B_O + 2, B_DRAIN = B_SF + 1, B_EX = B_DRAIN + 2,
+                       B_EM = B_EX + 1, NBAR = B_EM + 8;
+  // Exponents E of the last 8 pieces.  A softmax reads its piece's before it hands over its last P,
+  // and the conversion of V is at most NV tiles ahead of P.V and so NV + 1 pieces ahead of that.
+  static constexpr int NE = 8;
+  static_assert(NV + 1 < NE, "exponents kept");
+  static constexpr uint32_t MISC_OFF = BAR_OFF + NBAR * 8;   // tmem base, abort flag
+  static constexpr uint32_t EM_OFF = MISC_OFF + 8;           // E [NE], the warps' maxima [2][4]
+  static constexpr uint32_t BYTES = EM_OFF + NE * 4 + 32;
   static constexpr uint32_t ALLOC = BYTES + 1024;         // slack for 1024-byte alignment
   static_assert(ALLOC <= 227u * 1024u, "shared memory per CTA exceeds 227 KB");
 };
@@ -140,6 +248,21 @@ __device__ __forceinline__ float4 ld_shared_f4(uint32_t a) {
                      __uint_as_float(v.w));
 }
 
+// Bounded wait of this kernel: false once it has run for 2 s or another warp of the CTA has given up.
+// It only reports; the caller leaves its loops and raises the CTA's flag and the status at the end of
+// its role.  (The kernel has about twenty waits: with the whole of the general wait's slow path at
+// each of them its loops no longer fit the instruction cache.)
+__device__ __forceinline__ bool fp8_wait(uint32_t bar, uint32_t parity, volatile int* cta_abort) {
+  uint64_t t0 = 0;
+  for (uint32_t i = 0; !mbar_try(bar, parity);) {
+    if ((++i & 255u) != 0) continue;
+    const uint64_t now = globaltimer_ns();
+    if (i == 256u) t0 = now;
+    if (*cta_abort != 0 || now - t0 > kWaitTimeoutNs) return false;
+  }
+  return true;
+}
+
 template <int D>
 __global__ void __launch_bounds__(kFp8AttnThreads, 1)
     wf_attn_fp8_kernel(const __grid_constant__ AttnFp8Params p) {
@@ -152,40 +275,20 @@ __global__ void __launch_bounds__(kFp8AttnThreads, 1)
   uint8_t* const base_ptr = smem_raw + (base - raw);
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(base_ptr + L::MISC_OFF);
   volatile int* const cta_abort = reinterpret_cast<volatile int*>(base_ptr + L::MISC_OFF + 4);
-  int* const emax_slot = reinterpret_cast<int*>(base_ptr + L::MISC_OFF + 8);
+  int* const emax_slot = reinterpret_cast<int*>(base_ptr + L::EM_OFF);
   auto bar = [&](int i) -> uint32_t { return base + L::BAR_OFF + 8u * static_cast<uint32_t>(i); };
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // unit and part of this CTA: parts of a unit are neighbours; K/V heads go in groups, every row
-  // block of a group, longest first, heads fastest, before the next group
-  const int unit = static_cast<int>(blockIdx.x) / p.splits;
-  const int split = static_cast<int>(blockIdx.x) - unit * p.splits;
-  const int per_group = p.pairs * p.head_group;
-  const int hgrp = unit / per_group, in_group = unit - hgrp * per_group;
-  const int pair_all = in_group / p.head_group;
-  const int head = hgrp * p.head_group + in_group % p.head_group;
-  int seg = 0;
-  while (pair_all >= p.seg_pair_end[seg]) ++seg;
-  const int m0 = (pair_all - (seg > 0 ? p.seg_pair_end[seg - 1] : 0)) * (2 * kBM);
-  const int m_total = p.seg_rows[seg] * p.group;        // packed rows of the segment
-  const int nq = m0 + kBM < m_total ? 2 : 1;            // Q tiles with rows
-  const int n_max = p.seg_kv[seg];
-  const int n_tiles = (n_max + BN - 1) / BN;
-  const int kb = static_cast<int>(static_cast<int64_t>(split) * n_tiles / p.splits);
-  const int nk = static_cast<int>(static_cast<int64_t>(split + 1) * n_tiles / p.splits) - kb;
-
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the join waits by itself
-  const WaitCtx w{cta_abort, p.grid_abort, p.status, p.launch_id, 6 /* WF_ERR_TIMEOUT */,
-                  kWaitTimeoutNs};
   if (threadIdx.x == 0) {
     *cta_abort = (*reinterpret_cast<volatile unsigned*>(p.grid_abort) == p.launch_id) ? 1 : 0;
     for (int i = 0; i < L::NBAR; ++i) {
       uint32_t count = 1;
-      if (i == L::B_Q) count = 128u * nq;
+      if (i < L::B_KF) count = 128u;
       else if (i >= L::B_CE && i < L::B_VE) count = 128u;       // V codes read, V f16 written
       else if (i >= L::B_S && i < L::B_P) count = 2u;           // commit and the issuer itself
       else if (i >= L::B_P && i < L::B_O) count = 128u;
-      else if (i == L::B_SF) count = 4u;
+      else if (i == L::B_SF || i == L::B_EX) count = 4u;
       mbar_init(bar(i), count);
     }
     mbar_init_fence();
@@ -199,20 +302,32 @@ __global__ void __launch_bounds__(kFp8AttnThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const bool skip = *cta_abort != 0;
+  const WaitCtx w{cta_abort, p.grid_abort, p.status, p.launch_id, 6 /* WF_ERR_TIMEOUT */,
+                  kWaitTimeoutNs};
 
   if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kFp8RegSoftmax) : "memory");
     const int q = warp >> 2, wq = warp & 3;
-    if (!skip && q < nq) {
+    PieceList list(p);
+    Piece pc;
+    int done = 0;                      // tiles this Q tile has been through, over all pieces
+    int tiles = 0, n_piece = 0;        // tiles and pieces with keys of the CTA
+    bool ok = !skip;
+    while (ok && list.next(p, &pc)) {
+      const int nk = pc.nk;
+      const int it = tiles, piece = n_piece;
+      tiles += nk;
+      n_piece += nk > 0;
+      if (q >= pc.nq) continue;
       // ------------------------------------------------------------------ softmax warpgroups
       const int row = wq * 32 + lane;                       // row within the Q tile == TMEM lane
-      const int m = m0 + q * kBM + row;                     // packed row
-      const bool live = m < m_total;
-      const int64_t qrow = p.seg_row0[seg] + m / p.group;
-      const int qhead = head * p.group + m % p.group;
+      const int m = pc.m0 + q * kBM + row;                  // packed row
+      const bool live = m < pc.m_total;
+      const int64_t qrow = p.units.seg_row0[pc.seg] + m / p.units.group;
+      const int qhead = pc.head * p.units.group + m % p.units.group;
       const int64_t orow = qrow * p.Hq + qhead;
-      float sl2;
-      {
+      float sl2 = 0.f;
+      if (nk > 0) {
         // split this row into hi + lo e4m3 under 2^-e, and store both K-major
         uint4 x[D / 8];
         const uint4* src = reinterpret_cast<const uint4*>(p.q + orow * D);
@@ -247,7 +362,7 @@ __global__ void __launch_bounds__(kFp8AttnThreads, 1)
           st_shared_v4(lo_t + swz<D>(row, c), lw[0], lw[1], lw[2], lw[3]);
         }
         fence_proxy_async_smem();
-        mbar_arrive(bar(L::B_Q));
+        mbar_arrive(bar(L::B_Q + q));
       }
       const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
       const uint32_t tS = tmem + lane_off;                               // the shared S buffer
@@ -255,9 +370,9 @@ __global__ void __launch_bounds__(kFp8AttnThreads, 1)
       const uint32_t tO = tmem + lane_off + 256u + static_cast<uint32_t>(q * D);
       float m2 = -INFINITY;   // running reference of the base-2 logits
       float l = 0.f;          // running sum of exp2(t - m2 + kShift)
-      bool ok = true;
+      int e_v = 0;            // E of the piece
       for (int j = 0; j < nk; ++j) {
-        ok = __all_sync(0xffffffffu, mbar_wait(bar(L::B_S + q), j & 1, w));
+        ok = __all_sync(0xffffffffu, fp8_wait(bar(L::B_S + q), (done + j) & 1, cta_abort));
         if (!ok) break;
         tc_fence_after();
         float s[BN];
@@ -274,12 +389,12 @@ __global__ void __launch_bounds__(kFp8AttnThreads, 1)
           for (int c = 0; c < BN; ++c) s[c] = __uint_as_float(r[c]);
         }
         // logit factor of each block of 16 keys; kept positive so a masked column stays -inf
-        const uint32_t ks = base + L::KS_OFF + static_cast<uint32_t>(j % (2 * NK)) * 32u;
+        const uint32_t ks = base + L::KS_OFF + static_cast<uint32_t>((it + j) % (2 * NK)) * 32u;
         const float4 ka = ld_shared_f4(ks), kc = ld_shared_f4(ks + 16);
         float f[8] = {ka.x, ka.y, ka.z, ka.w, kc.x, kc.y, kc.z, kc.w};
 #pragma unroll
         for (int b = 0; b < 8; ++b) f[b] = fmaxf(f[b] * sl2, FLT_MIN);
-        const int lim = n_max - (kb + j) * BN;              // visible columns of this tile
+        const int lim = pc.n_max - (pc.kb + j) * BN;        // visible columns of this tile
         if (lim < BN) {
 #pragma unroll
           for (int c = 0; c < BN; ++c) s[c] = (c < lim) ? s[c] : -INFINITY;
@@ -315,7 +430,7 @@ __global__ void __launch_bounds__(kFp8AttnThreads, 1)
           acc[i & 3] = __fadd2_rn(acc[i & 3], e);
         }
         if (j > 0) {
-          ok = __all_sync(0xffffffffu, mbar_wait(bar(L::B_O + q), (j - 1) & 1, w));
+          ok = __all_sync(0xffffffffu, fp8_wait(bar(L::B_O + q), (done + j - 1) & 1, cta_abort));
           if (!ok) break;
           tc_fence_after();
           if (__any_sync(0xffffffffu, need)) {
@@ -338,6 +453,12 @@ __global__ void __launch_bounds__(kFp8AttnThreads, 1)
           const float2 t = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
           l = l * alpha + (t.x + t.y);
         }
+        if (j == nk - 1) {                                  // see NE
+          ok = __all_sync(0xffffffffu, fp8_wait(bar(L::B_EM + piece % L::NE),
+                                                 (piece / L::NE) & 1, cta_abort));
+          if (!ok) break;
+          e_v = emax_slot[piece % L::NE];
+        }
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(bar(L::B_P + q));
@@ -346,16 +467,16 @@ __global__ void __launch_bounds__(kFp8AttnThreads, 1)
       float inv = 0.f;
       if (nk > 0) {
         if (ok)
-          ok = __all_sync(0xffffffffu, mbar_wait(bar(L::B_O + q), (nk - 1) & 1, w) &&
-                                           mbar_wait(bar(L::B_EM), 0, w));
+          ok = __all_sync(0xffffffffu, fp8_wait(bar(L::B_O + q), (done + nk - 1) & 1, cta_abort));
         tc_fence_after();
-        if (ok) inv = l == 0.f ? 0.f : pow2f(*emax_slot - 7) / l;
+        if (ok) inv = l == 0.f ? 0.f : pow2f(e_v - 7) / l;
       }
+      done += nk;
       if (ok) {
-        // O / l: bf16 into `out`, or fp32 into the partials of a split; 0 and -inf for rows that
+        // O / l: bf16 into `out`, or fp32 into the workspace for a part; 0 and -inf for rows that
         // see no key (of the part)
-        const bool part = p.splits > 1;
-        const int64_t prow = static_cast<int64_t>(split) * p.T_q * p.Hq + orow;
+        const bool part = pc.slot >= 0;
+        const int64_t prow = static_cast<int64_t>(pc.slot) * kUnitTileRows + q * kBM + row;
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t r[32];
@@ -386,191 +507,206 @@ __global__ void __launch_bounds__(kFp8AttnThreads, 1)
           }
         }
         const float lse = l == 0.f ? -INFINITY : (m2 - kShift + __log2f(l)) * 0.69314718056f;
-        if (live && part)
-          p.part_lse[(static_cast<int64_t>(split) * p.Hq + qhead) * p.T_q + qrow] = lse;
-        else if (live && p.lse != nullptr)
-          p.lse[static_cast<int64_t>(qhead) * p.T_q + qrow] = lse;
+        if (live && part) p.part_lse[prow] = lse;
+        else if (live && p.lse != nullptr) p.lse[static_cast<int64_t>(qhead) * p.T_q + qrow] = lse;
       }
     }
+    if (!ok && !skip) raise_abort(w);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFp8RegOther) : "memory");
-    if (skip || nk == 0) {
-      // nothing to load or multiply
-    } else if (warp == 8 || warp == 11) {
-      // ------------------------------------------------------------------------ TMA producers
-      const bool is_k = warp == 8;
-      const CUtensorMap* map = is_k ? &p.tm_k : &p.tm_v;
-      const int ns = is_k ? NK : NC;
-      const int bf = is_k ? L::B_KF : L::B_CF, be = is_k ? L::B_KE : L::B_CE;
-      const uint32_t dst0 = base + (is_k ? L::K_OFF : L::C_OFF);
-      const int R = p.box_rows, nb = BN / R;               // page boxes per tile (<= BN / 16)
-      if (lane == 0) tma_prefetch_desc(map);
-      auto box_row = [&](int t, int b) -> int {            // past the pool (zeros) beyond n_max
-        const int tok = (kb + t) * BN + b * R;
-        if (b >= nb || t >= nk || tok >= n_max) return p.total_rows;
-        return fp8_row(p, tok);
-      };
-      // key scale of block `lane` of a tile (lanes 0..7)
-      auto key_scale = [&](int t) -> float {
-        const int tok = (kb + t) * BN + lane * 16;
-        if (!is_k || lane >= 8 || t >= nk || tok >= n_max) return 1.f;
-        const int r = fp8_row(p, tok);
-        const uint32_t b = __ldg(p.k_scale + static_cast<int64_t>(r / 16) * p.Hk + head);
-        return __uint_as_float(b << 23);
-      };
-      bool ok = true;
-      int issued = 0;
-      int coord_next = box_row(0, lane);                   // looked up one tile ahead
-      float ks_next = key_scale(0);
-      for (int j = 0; j < nk && ok; ++j) {
-        const int coord = coord_next;
-        const float ks = ks_next;
-        if (j + 1 < nk) {
-          coord_next = box_row(j + 1, lane);
-          ks_next = key_scale(j + 1);
-        }
-        int cb[BN / 16];
-#pragma unroll
-        for (int b = 0; b < BN / 16; ++b) cb[b] = __shfl_sync(0xffffffffu, coord, b);
-        const int slot = j % ns;
-        if (lane == 0) ok = mbar_wait(bar(be + slot), ((j / ns) & 1) ^ 1, w);
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (!ok) break;
-        if (is_k) {
-          // Scales of tile j go to slot j mod 2 NK.  The slot's last reader is tile j - 2 NK: this
-          // tile's K slot was freed by QK^T of tile j - NK, which waited for every softmax to have
-          // read S of the tile before it, and so to be done with the scales of all earlier ones.
-          if (lane < 8)
-            *reinterpret_cast<float*>(base_ptr + L::KS_OFF + (j % (2 * NK)) * 32 + lane * 4) = ks;
-          __syncwarp();
-        }
-        if (lane == 0) {
-          const uint32_t dst = dst0 + slot * L::CTILE;
-          mbar_arrive_expect_tx(bar(bf + slot), L::CTILE);
-#pragma unroll
-          for (int b = 0; b < BN / 16; ++b)
-            if (b < nb)
-              tma_load_3d(dst + static_cast<uint32_t>(b * R * D), map, 0, head, cb[b],
-                          bar(bf + slot));
-        }
-        issued = j + 1;
-      }
-      if (lane == 0) {
-        // every load this warp issued must land before shared memory is released
-        for (int r = 0; r < ns && r < issued; ++r) {
-          const int jl = issued - 1 - r;
-          mbar_wait_drain(bar(bf + jl % ns), (jl / ns) & 1);
-        }
-      }
-    } else if (warp >= 12) {
-      // -------------------------------------------------------------------------- V to f16
-      const int key = threadIdx.x - 384;                   // row of the tile this thread converts
-      const int first = kb * BN, last = min((kb + nk) * BN, n_max);
-      // the largest value exponent of this CTA's keys
-      int emax = 0;
-      for (int tok = first + 16 * key; tok < last; tok += 16 * 128)
-        emax = max(emax, static_cast<int>(__ldg(
-                             p.v_scale + static_cast<int64_t>(fp8_row(p, tok) / 16) * p.Hk + head)));
-      emax = __reduce_max_sync(0xffffffffu, emax);
-      int* const em = reinterpret_cast<int*>(base_ptr + L::MISC_OFF + 16);   // one per warp
-      if (lane == 0) em[warp - 12] = emax;
-      asm volatile("bar.sync 1, 128;" ::: "memory");
-      emax = max(max(em[0], em[1]), max(em[2], em[3])) - 127;
-      if (key == 0) {
-        *emax_slot = emax;
-        mbar_arrive(bar(L::B_EM));
-      }
-      auto factor = [&](int t) -> uint32_t {               // 2^(e_v - E + 7) as two f16
-        const int tok = (kb + t) * BN + key / 16 * 16;
-        if (t >= nk || tok >= n_max) return 0u;
-        const int e = static_cast<int>(__ldg(
-                          p.v_scale + static_cast<int64_t>(fp8_row(p, tok) / 16) * p.Hk + head)) -
-                      127 - emax + 7;
-        const uint32_t h = e >= -14 ? static_cast<uint32_t>(e + 15) << 10
-                           : e >= -24 ? 1u << (e + 24) : 0u;
-        return h | (h << 16);
-      };
-      uint32_t f_next = factor(0);
-      bool ok = true;
-      for (int j = 0; j < nk; ++j) {
-        const uint32_t f = f_next;
-        f_next = factor(j + 1);
-        const int cs = j % NC, vs = j % NV;
-        ok = mbar_wait(bar(L::B_CF + cs), (j / NC) & 1, w);
-        if (ok) ok = mbar_wait(bar(L::B_VE + vs), ((j / NV) & 1) ^ 1, w);
-        if (!__all_sync(0xffffffffu, ok)) break;
-        const uint32_t src = base + L::C_OFF + cs * L::CTILE;
-        const uint32_t dst = base + L::V_OFF + vs * L::VTILE;
-        const bool seen = (kb + j) * BN + key < n_max;     // else: zeros, whatever the bytes are
-#pragma unroll
-        for (int c = 0; c < D / 16; ++c) {
-          const uint4 v = ld_shared_v4(src + swz<D>(key, c));
-          const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-          uint32_t o[8];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            o[2 * i] = seen ? mul_f16x2(widen2(in[i]), f) : 0u;
-            o[2 * i + 1] = seen ? mul_f16x2(widen2_high(in[i]), f) : 0u;
+    // One loop over the pieces for all of these warps (it is inlined where it stands).  `it` counts key
+    // tiles over all pieces.
+    const bool producer = warp == 8 || warp == 11, issuer = warp == 9 || warp == 10;
+    bool ok = !skip && !(issuer && lane != 0);
+    int it = 0;
+    // TMA producers: K (with the key scales) or V codes
+    const bool is_k = warp == 8;
+    const CUtensorMap* const map = is_k ? &p.tm_k : &p.tm_v;
+    const int ns = is_k ? NK : NC;
+    const int bf = is_k ? L::B_KF : L::B_CF, be = is_k ? L::B_KE : L::B_CE;
+    if (producer && lane == 0) tma_prefetch_desc(map);
+    // V to f16: pieces so far, and the row of a tile this thread converts
+    int piece = 0;
+    const int key = threadIdx.x - 384;
+    // issuers: S-free phases consumed (nothing to wait for before the first S), pieces each Q tile has
+    // been part of, tiles Q tile 1 has been through (Q tile 0: all of them)
+    int sf = -1, n_q0 = 0, n_q1 = 0, n_p1 = 0;
+
+    PieceList list(p);
+    Piece pc;
+    while (ok && list.next(p, &pc)) {
+      const int nk = pc.nk;
+      if (nk == 0) continue;
+      if (producer) {
+        const int R = p.box_rows, nb = BN / R;             // page boxes per tile (<= BN / 16)
+        auto box_row = [&](int t, int b) -> int {          // past the pool (zeros) beyond n_max
+          const int tok = (pc.kb + t) * BN + b * R;
+          if (b >= nb || t >= nk || tok >= pc.n_max) return p.total_rows;
+          return fp8_row(p, tok);
+        };
+        // key scale of block `lane` of a tile (lanes 0..7)
+        auto key_scale = [&](int t) -> float {
+          const int tok = (pc.kb + t) * BN + lane * 16;
+          if (!is_k || lane >= 8 || t >= nk || tok >= pc.n_max) return 1.f;
+          const int r = fp8_row(p, tok);
+          const uint32_t b = __ldg(p.k_scale + static_cast<int64_t>(r / 16) * p.Hk + pc.head);
+          return __uint_as_float(b << 23);
+        };
+        int coord = box_row(0, lane);                      // looked up one tile ahead
+        float ks = key_scale(0);
+#pragma unroll 1
+        for (int j = 0; j < nk; ++j, ++it) {
+          const int slot = it % ns;
+          ok = fp8_wait(bar(be + slot), ((it / ns) & 1) ^ 1, cta_abort);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          if (is_k && lane < 8) {
+            // Scales of tile `it` go to slot it mod 2 NK, last read for tile it - 2 NK.  This tile's
+            // K slot was freed by QK^T of tile it - NK, issued after a softmax had read S of the tile
+            // before that one; a Q tile that is not part of those tiles' units holds P.V, and with
+            // it the other Q tile's next but one softmax, until it is done with its own last tile.
+            *reinterpret_cast<float*>(base_ptr + L::KS_OFF + (it % (2 * NK)) * 32 + lane * 4) = ks;
           }
-          // f16 channels 16 c .. 16 c + 15: pieces 2 c and 2 c + 1 of the 128-byte halves
-          const uint32_t half = dst + static_cast<uint32_t>(c / 4) * L::VHALF;
-          const int c2 = (c % 4) * 2;
-          st_shared_v4(half + swz<128>(key, c2), o[0], o[1], o[2], o[3]);
-          st_shared_v4(half + swz<128>(key, c2 + 1), o[4], o[5], o[6], o[7]);
+          __syncwarp();
+          if (lane == 0) mbar_arrive_expect_tx(bar(bf + slot), L::CTILE);
+          __syncwarp();
+          if (lane < nb)                                   // a box a lane
+            tma_load_3d(base + (is_k ? L::K_OFF : L::C_OFF) + slot * L::CTILE +
+                            static_cast<uint32_t>(lane * R * D),
+                        map, 0, pc.head, coord, bar(bf + slot));
+          __syncwarp();
+          if (j + 1 < nk) {
+            coord = box_row(j + 1, lane);
+            ks = key_scale(j + 1);
+          }
         }
-        fence_proxy_async_smem();
-        mbar_arrive(bar(L::B_VF + vs));
-        mbar_arrive(bar(L::B_CE + cs));
-      }
-    } else if (lane == 0) {
-      // ---------------------------------------------------------------------- MMA issuers
-      constexpr uint32_t idesc_qk = idesc_e4m3_f32(kBM, BN);
-      constexpr uint32_t idesc_pv = idesc_f16_f32_bmn(kBM, D);
-      bool ok = true;
-      if (warp == 9) {
+      } else if (warp >= 12) {
+        const int first = pc.kb * BN, last = min((pc.kb + nk) * BN, pc.n_max);
+        auto exponent = [&](int tok) -> int {              // value scale of a token's block, biased
+          return __ldg(p.v_scale + static_cast<int64_t>(fp8_row(p, tok) / 16) * p.Hk + pc.head);
+        };
+        // the largest value exponent of this piece's keys
+        int emax = 0;
+#pragma unroll 1
+        for (int tok = first + 16 * key; tok < last; tok += 16 * 128) emax = max(emax, exponent(tok));
+        emax = __reduce_max_sync(0xffffffffu, emax);
+        // One word per warp, in turn for even and odd pieces: a warp is at most one phase ahead.
+        // (An mbarrier and no bar.sync: a warp whose wait runs out must not leave others waiting.)
+        int* const em = emax_slot + L::NE + 4 * (piece & 1);
+        if (lane == 0) {
+          em[warp - 12] = emax;
+          mbar_arrive(bar(L::B_EX));
+        }
+        ok = __all_sync(0xffffffffu, fp8_wait(bar(L::B_EX), piece & 1, cta_abort));
+        if (!ok) break;
+        emax = max(max(em[0], em[1]), max(em[2], em[3])) - 127;
+        if (key == 0) {
+          emax_slot[piece % L::NE] = emax;
+          mbar_arrive(bar(L::B_EM + piece % L::NE));
+        }
+        ++piece;
+        auto factor = [&](int t) -> uint32_t {             // 2^(e_v - E + 7) as two f16
+          const int tok = (pc.kb + t) * BN + key / 16 * 16;
+          if (t >= nk || tok >= pc.n_max) return 0u;
+          const int e = exponent(tok) - 127 - emax + 7;
+          const uint32_t h = e >= -14 ? static_cast<uint32_t>(e + 15) << 10
+                             : e >= -24 ? 1u << (e + 24) : 0u;
+          return h | (h << 16);
+        };
+        uint32_t f_next = factor(0);
+#pragma unroll 1
+        for (int j = 0; j < nk; ++j, ++it) {
+          const uint32_t f = f_next;
+          f_next = factor(j + 1);
+          const int cs = it % NC, vs = it % NV;
+          ok = fp8_wait(bar(L::B_CF + cs), (it / NC) & 1, cta_abort) &&
+               fp8_wait(bar(L::B_VE + vs), ((it / NV) & 1) ^ 1, cta_abort);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          const uint32_t src = base + L::C_OFF + cs * L::CTILE;
+          const uint32_t dst = base + L::V_OFF + vs * L::VTILE;
+          const bool seen = (pc.kb + j) * BN + key < pc.n_max;   // else zeros, whatever the bytes
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c) {
+            const uint4 v = ld_shared_v4(src + swz<D>(key, c));
+            const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+            uint32_t o[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              o[2 * i] = seen ? mul_f16x2(widen2(in[i]), f) : 0u;
+              o[2 * i + 1] = seen ? mul_f16x2(widen2_high(in[i]), f) : 0u;
+            }
+            // f16 channels 16 c .. 16 c + 15: pieces 2 c and 2 c + 1 of the 128-byte halves
+            const uint32_t half = dst + static_cast<uint32_t>(c / 4) * L::VHALF;
+            const int c2 = (c % 4) * 2;
+            st_shared_v4(half + swz<128>(key, c2), o[0], o[1], o[2], o[3]);
+            st_shared_v4(half + swz<128>(key, c2 + 1), o[4], o[5], o[6], o[7]);
+          }
+          fence_proxy_async_smem();
+          mbar_arrive(bar(L::B_VF + vs));
+          mbar_arrive(bar(L::B_CE + cs));
+        }
+      } else if (warp == 9) {
         // S(j, q) = (hi_q + lo_q) K_j^T: 2 D/32 steps of 32 channels into the shared S columns
-        int sf = 0;           // S-free phases consumed
-        ok = mbar_wait(bar(L::B_Q), 0, w);
-        for (int j = 0; ok && j < nk; ++j) {
+        constexpr uint32_t idesc = idesc_e4m3_f32(kBM, BN);
+        ok = fp8_wait(bar(L::B_Q), (n_q0++) & 1, cta_abort);
+        if (ok && pc.nq > 1) ok = fp8_wait(bar(L::B_Q + 1), (n_q1++) & 1, cta_abort);
+#pragma unroll 1
+        for (int j = 0; ok && j < nk; ++j, ++it) {
           const uint64_t dk =
-              smem_desc_codes<D>(base + L::K_OFF + static_cast<uint32_t>(j % NK) * L::CTILE);
-          ok = mbar_wait(bar(L::B_KF + j % NK), (j / NK) & 1, w);
-          for (int q = 0; ok && q < nq; ++q) {
-            if (j > 0 || q > 0) ok = mbar_wait(bar(L::B_SF), (sf++) & 1, w);
+              smem_desc_codes<D>(base + L::K_OFF + static_cast<uint32_t>(it % NK) * L::CTILE);
+          ok = fp8_wait(bar(L::B_KF + it % NK), (it / NK) & 1, cta_abort);
+#pragma unroll 1
+          for (int q = 0; ok && q < pc.nq; ++q) {
+            if (sf >= 0) ok = fp8_wait(bar(L::B_SF), sf & 1, cta_abort);
+            ++sf;
             if (!ok) break;
             tc_fence_after();
             const uint64_t dq = smem_desc_codes<D>(base + L::Q_OFF + 2u * q * L::QTERM);
 #pragma unroll
             for (int kk = 0; kk < 2 * (D / 32); ++kk)
               umma_ss_f8(tmem, dq + ((kk / (D / 32) * L::QTERM + kk % (D / 32) * 32) >> 4),
-                         dk + ((kk % (D / 32) * 32) >> 4), idesc_qk, kk > 0 ? 1u : 0u);
+                         dk + ((kk % (D / 32) * 32) >> 4), idesc, kk > 0 ? 1u : 0u);
             umma_commit(bar(L::B_S + q));
             // a second, plain arrival: it hands on what this thread saw with K_j, the key scales
             mbar_arrive(bar(L::B_S + q));
           }
-          if (ok) umma_commit(bar(L::B_KE + j % NK));              // K_j free
+          if (ok) umma_commit(bar(L::B_KE + it % NK));               // K_j free
         }
       } else {
         // O_q += P_q(j) V_j
-        for (int j = 0; ok && j < nk; ++j) {
+        constexpr uint32_t idesc = idesc_f16_f32_bmn(kBM, D);
+#pragma unroll 1
+        for (int j = 0; ok && j < nk; ++j, ++it) {
           const uint64_t dv = smem_desc_sw128(
-              base + L::V_OFF + static_cast<uint32_t>(j % NV) * L::VTILE, L::VHALF, 1024);
-          ok = mbar_wait(bar(L::B_VF + j % NV), (j / NV) & 1, w);
-          for (int q = 0; ok && q < nq; ++q) {
-            ok = mbar_wait(bar(L::B_P + q), j & 1, w);
+              base + L::V_OFF + static_cast<uint32_t>(it % NV) * L::VTILE, L::VHALF, 1024);
+          ok = fp8_wait(bar(L::B_VF + it % NV), (it / NV) & 1, cta_abort);
+#pragma unroll 1
+          for (int q = 0; ok && q < pc.nq; ++q) {
+            ok = fp8_wait(bar(L::B_P + q), (q ? n_p1++ : it) & 1, cta_abort);
             if (!ok) break;
             tc_fence_after();
             const uint32_t pa = tmem + 128u + static_cast<uint32_t>(q * 64);
             const uint32_t od = tmem + 256u + static_cast<uint32_t>(q * D);
 #pragma unroll
             for (int kk = 0; kk < BN / 16; ++kk)
-              umma_ts(od, pa + 8u * kk, dv + ((kk * 2048u) >> 4), idesc_pv,
+              umma_ts(od, pa + 8u * kk, dv + ((kk * 2048u) >> 4), idesc,
                       (j > 0 || kk > 0) ? 1u : 0u);
             umma_commit(bar(L::B_O + q));
           }
-          if (ok) umma_commit(bar(L::B_VE + j % NV));              // V_j free
+          if (ok) umma_commit(bar(L::B_VE + it % NV));               // V_j free
         }
       }
+    }
+    if (!ok && !skip && !(issuer && lane != 0)) raise_abort(w);
+    if (producer && lane == 0) {
+      // every load this warp issued must land before shared memory is released
+      for (int r = 0; r < ns && r < it; ++r) {
+        const int jl = it - 1 - r;
+        mbar_wait_drain(bar(bf + jl % ns), (jl / ns) & 1);
+      }
+    }
+    if (issuer && lane == 0) {
       // every MMA this thread issued must complete before TMEM is released
       umma_commit(bar(L::B_DRAIN + (warp - 9)));
       mbar_wait_drain(bar(L::B_DRAIN + (warp - 9)), 0);
@@ -583,6 +719,70 @@ __global__ void __launch_bounds__(kFp8AttnThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+}
+
+// Joins the pieces of the units that were cut: out = sum_s exp(lse_s - lse) O_s.  One warp per packed
+// row; grid (cut units, row groups).  The parts of a cut unit lie in consecutive slots.
+struct Fp8JoinParams {
+  Fp8Units units;
+  const float* part_o;
+  const float* part_lse;
+  __nv_bfloat16* out;
+  float* lse;
+  int T_q, Hq;
+  int unit[kFp8MaxCtas];
+  int slot[kFp8MaxCtas];     // of the unit's first part
+  int parts[kFp8MaxCtas];
+};
+
+constexpr int kPieceJoinThreads = 256;
+
+template <int D>
+__global__ void __launch_bounds__(kPieceJoinThreads)
+    wf_piece_join_kernel(const __grid_constant__ Fp8JoinParams p) {
+  constexpr int PER = D / 32;
+  const int lane = threadIdx.x & 31;
+  const UnitAt at = unit_at(p.units, p.unit[blockIdx.x]);
+  const int r = static_cast<int>(blockIdx.y) * (kPieceJoinThreads / 32) + (threadIdx.x >> 5);
+  const int m = at.m0 + r;
+  if (m >= p.units.seg_rows[at.seg] * p.units.group) return;
+  const int slot0 = p.slot[blockIdx.x], parts = p.parts[blockIdx.x];
+  const auto prow = [&](int s) -> int64_t {
+    return static_cast<int64_t>(slot0 + s) * kUnitTileRows + r;
+  };
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  float top = -INFINITY;
+  for (int s = lane; s < parts; s += 32) top = fmaxf(top, p.part_lse[prow(s)]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const float ref = top == -INFINITY ? 0.f : top;
+  float total = 0.f, acc[PER];
+#pragma unroll
+  for (int c = 0; c < PER; ++c) acc[c] = 0.f;
+#pragma unroll 4
+  for (int s = 0; s < parts; ++s) {
+    const float wt = expf(p.part_lse[prow(s)] - ref);
+    const float* src = p.part_o + prow(s) * D + lane * PER;
+    float x[PER];
+    if (PER == 4) {
+      const float4 v = *reinterpret_cast<const float4*>(src);
+      x[0] = v.x, x[1] = v.y, x[PER - 2] = v.z, x[PER - 1] = v.w;
+    } else {
+      const float2 v = *reinterpret_cast<const float2*>(src);
+      x[0] = v.x, x[1] = v.y;
+    }
+    total += wt;
+#pragma unroll
+    for (int c = 0; c < PER; ++c) acc[c] = fmaf(wt, x[c], acc[c]);
+  }
+  const float inv = total == 0.f ? 0.f : 1.f / total;
+  const int64_t row = p.units.seg_row0[at.seg] + m / p.units.group;
+  const int h = at.head * p.units.group + m % p.units.group;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + (row * p.Hq + h) * D + lane * PER);
+#pragma unroll
+  for (int c = 0; c < PER / 2; ++c) dst[c] = pack_bf16x2(acc[2 * c] * inv, acc[2 * c + 1] * inv);
+  if (lane == 0 && p.lse != nullptr)
+    p.lse[static_cast<int64_t>(h) * p.T_q + row] = total == 0.f ? -INFINITY : ref + logf(total);
 }
 
 }  // namespace wfk

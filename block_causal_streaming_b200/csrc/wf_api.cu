@@ -1666,87 +1666,158 @@ int segment_list(const wf_segments_t* seg, SegmentList* out) {
 }
 
 // What a call launches.  Few packed rows (query rows x heads of a K/V head's group) in every
-// segment: tiles of 8 nt rows on the matrix instructions that read registers; else row blocks of
-// 256 on the tensor core's own memory.  Segments never share a tile or a row block.
+// segment: tiles of 8 nt rows on the matrix instructions that read registers, each in `splits` key
+// parts; else row blocks of 256 on the tensor core's own memory, spread over the SMs.  Segments never
+// share a tile or a row block.
 struct Fp8Plan {
   bool few = true;
-  int nt = 1, splits = 1;
-  int tiles = 0;                    // tiles or row blocks
-  int order[WF_MAX_CHUNKS];         // segments in dispatch order
-  int tile_end[WF_MAX_CHUNKS];      // in that order
+  // few rows
+  int nt = 1, splits = 1, tiles = 0;
+  int tile_end[WF_MAX_CHUNKS];
+  // row blocks
+  int ctas = 0, n_units = 0, n_whole = 0, n_blank = 0, n_cut = 0, n_slots = 0;
+  wfk::Fp8Units units;
+  int share_unit[wfk::kFp8MaxCtas], share_tile[wfk::kFp8MaxCtas], share_tiles[wfk::kFp8MaxCtas],
+      share_slot[wfk::kFp8MaxCtas];
+  int cut_unit[wfk::kFp8MaxCtas], cut_slot[wfk::kFp8MaxCtas], cut_parts[wfk::kFp8MaxCtas];
 };
 
-constexpr int kFewRows = 32;        // packed rows up to which the few-row kernel runs
-constexpr int kMaxRowBlockSplits = 64;
+// Packed rows up to which the few-row kernel runs.  Measured, few / row blocks, one call in a graph:
+// 37 440 keys x 12 heads, 16 rows 35 / 52 us, 32 rows 50 / 54, 48 rows 80 / 55; 8192 keys x 8 heads,
+// 32 rows 18 / 20, 64 rows 23 / 21.
+constexpr int kFewRows = 32;
 
-// Key parts of each row block: the count a model of the grid finds shortest, in times of a key
-// tile.  Blocks go out most keys first, one to an SM at a time; each costs its tiles and about 2.5
-// for its start and end; the join of a split costs about kMergePerPart for a million parts of rows.
-// Blocks that see no key come last and cost next to nothing.
-int fp8_row_block_splits(const SegmentList& sl, const Fp8Plan& plan, int Hq, int Hk,
-                         int num_sms) {
-  int seen = 0;                                            // row blocks that see a key
-  for (int i = 0; i < sl.n; ++i)
-    if (sl.kv[plan.order[i]] > 0) seen = plan.tile_end[i];
-  const int64_t units = static_cast<int64_t>(seen) * Hk;
-  if (units >= 2 * static_cast<int64_t>(num_sms)) return 1;
-  int best = 1;
-  double best_cost = 0;
-  const int most = std::max((sl.max_kv + wfk::kBN - 1) / wfk::kBN, 1);
-  for (int S = 1; S <= std::min(kMaxRowBlockSplits, most); ++S) {
-    double cost = S > 1 ? kMergePerPart * sl.t_q * Hq * S / 1e6 : 0;
-    int seg = 0;
-    for (int64_t u = 0; u < units * S; u += num_sms) {     // one wave after the other
-      const int64_t block = u / S / Hk;
-      while (block >= plan.tile_end[seg]) ++seg;
-      const int tiles = (sl.kv[plan.order[seg]] + wfk::kBN - 1) / wfk::kBN;
-      cost += (tiles + S - 1) / S + kCtaOverhead;
-    }
-    if (S == 1 || cost < best_cost) {
-      best = S;
-      best_cost = cost;
+// Spreads the key tiles of the row blocks over `ctas` CTAs (see the kernel): `n_whole` units go out
+// whole, unit k ctas + i to CTA i; the tiles of the others fill the CTAs up to one level, in unit
+// order.  Units of unequal length can leave whole turns uneven by more than the rest can fill: turns
+// are given up to the rest until the fullest CTA is within 2 % of an even share.
+void fp8_shares(Fp8Plan* pl, int num_sms) {
+  const wfk::Fp8Units& u = pl->units;
+  const auto tiles = [&](int unit) {
+    return (u.seg_kv[wfk::unit_at(u, unit).seg] + wfk::kBN - 1) / wfk::kBN;
+  };
+  int64_t total = 0;
+  std::vector<int> len(static_cast<size_t>(pl->n_units));
+  for (int i = 0; i < pl->n_units; ++i) total += len[static_cast<size_t>(i)] = tiles(i);
+  const int G = static_cast<int>(std::min<int64_t>(
+      std::min(num_sms, wfk::kFp8MaxCtas), std::max<int64_t>({total, pl->n_blank, 1})));
+  pl->ctas = G;
+  std::vector<int64_t> load(static_cast<size_t>(G), 0);
+  int turns = pl->n_units / G;
+  int64_t rest = total, most = 0;
+  for (int i = 0; i < turns * G; ++i) {
+    load[static_cast<size_t>(i % G)] += len[static_cast<size_t>(i)];
+    rest -= len[static_cast<size_t>(i)];
+  }
+  for (;; --turns) {
+    most = *std::max_element(load.begin(), load.end());
+    if (turns == 0 || most * G <= total + total / 50) break;
+    for (int i = (turns - 1) * G; i < turns * G; ++i) {
+      load[static_cast<size_t>(i % G)] -= len[static_cast<size_t>(i)];
+      rest += len[static_cast<size_t>(i)];
     }
   }
-  return best;
+  pl->n_whole = turns * G;
+  // least level X with sum max(0, X - load) >= rest
+  int64_t level = 0, above = most + rest;
+  while (level < above) {
+    const int64_t x = (level + above) / 2;
+    int64_t room = 0;
+    for (int64_t l : load) room += std::max<int64_t>(0, x - l);
+    if (room >= rest) above = x;
+    else level = x + 1;
+  }
+  int unit = pl->n_whole, at = 0;
+  for (int i = 0; i < G; ++i) {
+    int64_t room = std::max<int64_t>(0, level - load[static_cast<size_t>(i)]);
+    pl->share_unit[i] = unit;
+    pl->share_tile[i] = at;
+    pl->share_slot[i] = pl->n_slots;
+    int64_t take = 0;
+    while (room > 0 && unit < pl->n_units) {
+      const int n = len[static_cast<size_t>(unit)];
+      const int piece = static_cast<int>(std::min<int64_t>(n - at, room));
+      if (piece < n) {                             // part of a unit
+        if (at == 0) {
+          pl->cut_unit[pl->n_cut] = unit;
+          pl->cut_slot[pl->n_cut] = pl->n_slots;
+          pl->cut_parts[pl->n_cut++] = 1;
+        } else {
+          ++pl->cut_parts[pl->n_cut - 1];
+        }
+        ++pl->n_slots;
+      }
+      room -= piece;
+      take += piece;
+      at += piece;
+      if (at == n) {
+        ++unit;
+        at = 0;
+      }
+    }
+    pl->share_tiles[i] = static_cast<int>(take);
+  }
 }
 
 int fp8_plan(const SegmentList& sl, int Hq, int Hk, int splits, int num_sms, Fp8Plan* plan) {
   const int64_t group = Hq / Hk;
   int64_t most = 0, tiles = 0;
-  for (int i = 0; i < sl.n; ++i) {
-    most = std::max(most, sl.rows(i) * group);
-    plan->order[i] = i;
-  }
+  for (int i = 0; i < sl.n; ++i) most = std::max(most, sl.rows(i) * group);
   if (most > INT32_MAX) return WF_ERR_SHAPE;
   plan->few = most <= kFewRows;
-  plan->nt = most > 16 ? 4 : most > 8 ? 2 : 1;
-  if (!plan->few)
-    std::stable_sort(plan->order, plan->order + sl.n,
-                     [&](int a, int b) { return sl.kv[a] > sl.kv[b]; });
-  const int64_t per_tile = plan->few ? 8 * plan->nt : kUnitRows;
+  if (plan->few) {
+    plan->nt = most > 16 ? 4 : most > 8 ? 2 : 1;
+    for (int i = 0; i < sl.n; ++i) {
+      tiles += (sl.rows(i) * group + 8 * plan->nt - 1) / (8 * plan->nt);
+      plan->tile_end[i] = static_cast<int>(tiles);
+    }
+    if (tiles * Hk * kMaxFp8Splits > INT32_MAX) return WF_ERR_SHAPE;
+    plan->tiles = static_cast<int>(tiles);
+    if (splits == 0) {
+      // as many parts as there are places for CTAs (two an SM, one with more than 16 rows)
+      const int64_t places = static_cast<int64_t>(num_sms) * (plan->nt <= 2 ? 2 : 1);
+      splits = static_cast<int>(std::max<int64_t>(1, places / (tiles * Hk)));
+    }
+    // parts are runs of blocks of 16 keys, one at least for every warp
+    const int blocks = (sl.max_kv + 16 * wfk::kFewWarps - 1) / (16 * wfk::kFewWarps);
+    plan->splits = std::max(1, std::min({splits, kMaxFp8Splits, blocks}));
+    return WF_OK;
+  }
+  int order[WF_MAX_CHUNKS];                       // segments, most keys first
+  for (int i = 0; i < sl.n; ++i) order[i] = i;
+  std::stable_sort(order, order + sl.n, [&](int a, int b) { return sl.kv[a] > sl.kv[b]; });
+  wfk::Fp8Units& u = plan->units;
+  u.Hk = Hk;
+  u.group = static_cast<int>(group);
+  u.head_group = head_group(Hk);
+  u.pairs = 0;
   for (int i = 0; i < sl.n; ++i) {
-    tiles += (sl.rows(plan->order[i]) * group + per_tile - 1) / per_tile;
-    plan->tile_end[i] = static_cast<int>(std::min<int64_t>(tiles, INT32_MAX));
+    const int g = order[i];
+    tiles += (sl.rows(g) * group + wfk::kUnitTileRows - 1) / wfk::kUnitTileRows;
+    if (tiles * Hk > INT32_MAX / 2) return WF_ERR_SHAPE;
+    u.seg_pair_end[i] = static_cast<int>(tiles);
+    u.seg_row0[i] = g > 0 ? sl.row_end[g - 1] : 0;
+    u.seg_rows[i] = sl.rows(g);
+    u.seg_kv[i] = sl.kv[g];
+    if (sl.kv[g] > 0) u.pairs = static_cast<int>(tiles);
   }
-  if (tiles * Hk * kMaxFp8Splits > INT32_MAX) return WF_ERR_SHAPE;
-  plan->tiles = static_cast<int>(tiles);
-  // parts are runs of 16 keys, or of 128; a part keeps a block for every warp
-  const int blocks = plan->few ? (sl.max_kv + 16 * wfk::kFewWarps - 1) / (16 * wfk::kFewWarps)
-                               : (sl.max_kv + wfk::kBN - 1) / wfk::kBN;
-  if (splits == 0 && plan->few) {
-    // as many parts as there are places for CTAs (two an SM, one with more than 16 rows)
-    const int64_t places = static_cast<int64_t>(num_sms) * (plan->nt <= 2 ? 2 : 1);
-    splits = static_cast<int>(std::max<int64_t>(1, places / (tiles * Hk)));
-  } else if (splits == 0) {
-    splits = fp8_row_block_splits(sl, *plan, Hq, Hk, num_sms);
+  plan->n_units = u.pairs * Hk;
+  plan->n_blank = (static_cast<int>(tiles) - u.pairs) * Hk;
+  if (splits == 1) {                              // every unit whole
+    plan->ctas = std::min({num_sms, wfk::kFp8MaxCtas, plan->n_units + plan->n_blank});
+    plan->n_whole = plan->n_units;
+    for (int i = 0; i < plan->ctas; ++i)
+      plan->share_unit[i] = plan->share_tile[i] = plan->share_tiles[i] = plan->share_slot[i] = 0;
+  } else {
+    fp8_shares(plan, num_sms);
   }
-  plan->splits = std::max(1, std::min({splits, kMaxFp8Splits, blocks}));
   return WF_OK;
 }
 
 size_t fp8_workspace_bytes(const SegmentList& sl, const Fp8Plan& plan, int Hq, int D) {
-  if (plan.splits <= 1) return 0;
-  const size_t rows = static_cast<size_t>(plan.splits) * sl.t_q * Hq;
+  size_t rows = 0;
+  if (plan.few && plan.splits > 1) rows = static_cast<size_t>(plan.splits) * sl.t_q * Hq;
+  if (!plan.few) rows = static_cast<size_t>(plan.n_slots) * wfk::kUnitTileRows;
   return align256(rows * D * sizeof(float)) + align256(rows * sizeof(float));
 }
 
@@ -1757,31 +1828,32 @@ int launch_few(const wfk::AttnFewParams& p, cudaStream_t s) {
   return cudaGetLastError() == cudaSuccess ? WF_OK : WF_ERR_CUDA;
 }
 
-// (row, head) pairs up to which a block each joins the parts; above, a warp each (the merge kernel).
-// Measured, join / merge, keys 37 440 x 12 heads: 1536 pairs 61 / 64 us the call, 6144 pairs
-// 135 / 128; keys 8192 x 8 heads: 384 pairs 18.1 / 21.8, 2048 pairs 33.6 / 32.4.
-constexpr int kJoinRows = 2048;
-
-// The join of a launch's parts, its blocks launched while that one still runs.
-template <int D>
-int launch_join(const wfk::AttnFewParams& p, cudaStream_t s) {
+// A launch whose blocks may take their places while the kernel before it still runs.
+template <typename... Args, typename... Given>
+int launch_early(void (*kernel)(Args...), dim3 grid, int threads, cudaStream_t s, Given... given) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.T_q) * p.Hq);
-  cfg.blockDim = dim3(wfk::kJoinThreads);
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
   cfg.stream = s;
   cudaLaunchAttribute attr = {};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  static_assert(kMaxFp8Splits <= wfk::kMaxJoin, "parts");
-  if (cudaLaunchKernelEx(&cfg, wfk::wf_join_kernel<D>, static_cast<const float*>(p.part_o),
-                         static_cast<const float*>(p.part_lse), p.splits, p.T_q, p.Hq, p.out,
-                         p.lse) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, kernel, static_cast<Args>(given)...) != cudaSuccess) {
     cudaGetLastError();
     return WF_ERR_CUDA;
   }
   return WF_OK;
+}
+
+// The join of the few-row kernel's parts.
+template <int D>
+int launch_join(const wfk::AttnFewParams& p, cudaStream_t s) {
+  static_assert(kMaxFp8Splits <= wfk::kMaxJoin, "parts");
+  return launch_early(wfk::wf_join_kernel<D>, dim3(static_cast<unsigned>(p.T_q) * p.Hq),
+                      wfk::kJoinThreads, s, p.part_o, p.part_lse, p.splits, p.T_q, p.Hq, p.out,
+                      p.lse);
 }
 
 // e4m3 tensor (D, H, rows), row stride H * D bytes, box (D, 1, box_rows), swizzled over D bytes.
@@ -1800,8 +1872,7 @@ bool encode_codes(CUtensorMap* map, const void* ptr, int D, int H, int64_t rows,
 }
 
 template <int D>
-int launch_fp8_blocks(const wfk::AttnFewParams& a, const SegmentList& sl, const Fp8Plan& plan,
-                      cudaStream_t s) {
+int launch_fp8_blocks(const wfk::AttnFewParams& a, const Fp8Plan& plan, cudaStream_t s) {
   alignas(64) wfk::AttnFp8Params p;
   std::memset(&p, 0, sizeof(p));
   p.tm_k = a.tm_k;
@@ -1822,24 +1893,36 @@ int launch_fp8_blocks(const wfk::AttnFewParams& a, const SegmentList& sl, const 
   p.T_q = a.T_q;
   p.Hq = a.Hq;
   p.Hk = a.Hk;
-  p.group = a.group;
   p.page_size = a.page_size;
   p.num_pages = a.num_pages;
-  p.splits = plan.splits;
-  p.head_group = head_group(a.Hk);
-  p.pairs = plan.tiles;
   p.sl2 = a.sl2;
-  for (int i = 0; i < sl.n; ++i) {
-    const int g = plan.order[i];
-    p.seg_pair_end[i] = plan.tile_end[i];
-    p.seg_row0[i] = g > 0 ? sl.row_end[g - 1] : 0;
-    p.seg_rows[i] = sl.rows(g);
-    p.seg_kv[i] = sl.kv[g];
-  }
-  auto kernel = wfk::wf_attn_fp8_kernel<D>;
-  const unsigned grid = static_cast<unsigned>(p.pairs) * p.Hk * p.splits;
-  kernel<<<grid, wfk::kFp8AttnThreads, wfk::AttnFp8Smem<D>::ALLOC, s>>>(p);
-  return cudaGetLastError() == cudaSuccess ? WF_OK : WF_ERR_CUDA;
+  p.units = plan.units;
+  p.n_units = plan.n_units;
+  p.n_whole = plan.n_whole;
+  p.n_blank = plan.n_blank;
+  std::memcpy(p.share_unit, plan.share_unit, sizeof(int) * plan.ctas);
+  std::memcpy(p.share_tile, plan.share_tile, sizeof(int) * plan.ctas);
+  std::memcpy(p.share_tiles, plan.share_tiles, sizeof(int) * plan.ctas);
+  std::memcpy(p.share_slot, plan.share_slot, sizeof(int) * plan.ctas);
+  wfk::wf_attn_fp8_kernel<D>
+      <<<static_cast<unsigned>(plan.ctas), wfk::kFp8AttnThreads, wfk::AttnFp8Smem<D>::ALLOC, s>>>(p);
+  if (cudaGetLastError() != cudaSuccess) return WF_ERR_CUDA;
+  if (plan.n_cut == 0) return WF_OK;
+  wfk::Fp8JoinParams j;
+  j.units = plan.units;
+  j.part_o = a.part_o;
+  j.part_lse = a.part_lse;
+  j.out = a.out;
+  j.lse = a.lse;
+  j.T_q = a.T_q;
+  j.Hq = a.Hq;
+  std::memcpy(j.unit, plan.cut_unit, sizeof(int) * plan.n_cut);
+  std::memcpy(j.slot, plan.cut_slot, sizeof(int) * plan.n_cut);
+  std::memcpy(j.parts, plan.cut_parts, sizeof(int) * plan.n_cut);
+  const int rows = wfk::kPieceJoinThreads / 32;
+  return launch_early(wfk::wf_piece_join_kernel<D>,
+                      dim3(static_cast<unsigned>(plan.n_cut), wfk::kUnitTileRows / rows),
+                      wfk::kPieceJoinThreads, s, j);
 }
 
 }  // namespace
@@ -1852,12 +1935,10 @@ size_t wf_attn_fp8_block_workspace_size(const wf_segments_t* segments, int num_q
   if (num_q_heads < 1 || num_kv_heads < 1 || num_q_heads % num_kv_heads != 0 || splits < 0 ||
       (head_dim != 64 && head_dim != 128) || segment_list(segments, &sl) != WF_OK || sl.t_q == 0)
     return 0;
-  int sms = 0;
-  if (splits == 0) {
-    DeviceState* d = nullptr;
-    if (device_state(&d) != WF_OK) return 0;
-    sms = d->num_sms;
-  }
+  if (splits == 1) return 0;                      // nothing is cut
+  DeviceState* d = nullptr;
+  if (device_state(&d) != WF_OK) return 0;
+  const int sms = d->num_sms;
   Fp8Plan plan;
   if (fp8_plan(sl, num_q_heads, num_kv_heads, splits, sms, &plan) != WF_OK) return 0;
   return fp8_workspace_bytes(sl, plan, num_q_heads, head_dim);
@@ -1915,19 +1996,23 @@ int wf_attn_forward_fp8_block(const void* q, int num_q_heads,
   p.group = num_q_heads / Hk;
   p.page_size = ps;
   p.num_pages = kv_pages->num_pages;
-  p.splits = plan.splits;
-  p.tiles = plan.tiles;
   p.sl2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
-  p.nseg = sl.n;
-  for (int i = 0; i < sl.n; ++i) {
-    p.seg_tile_end[i] = plan.tile_end[i];
-    p.seg_row_end[i] = sl.row_end[i];
-    p.seg_kv[i] = sl.kv[i];
+  if (plan.few) {
+    p.splits = plan.splits;
+    p.tiles = plan.tiles;
+    p.nseg = sl.n;
+    for (int i = 0; i < sl.n; ++i) {
+      p.seg_tile_end[i] = plan.tile_end[i];
+      p.seg_row_end[i] = sl.row_end[i];
+      p.seg_kv[i] = sl.kv[i];
+    }
   }
-  if (plan.splits > 1) {
+  const size_t need = fp8_workspace_bytes(sl, plan, num_q_heads, D);
+  if (need > 0) {
     if (workspace == nullptr || !aligned16(workspace)) return WF_ERR_INVALID_ARG;
-    if (workspace_bytes < fp8_workspace_bytes(sl, plan, num_q_heads, D)) return WF_ERR_CAPACITY;
-    const size_t rows = static_cast<size_t>(plan.splits) * sl.t_q * num_q_heads;
+    if (workspace_bytes < need) return WF_ERR_CAPACITY;
+    const size_t rows = plan.few ? static_cast<size_t>(plan.splits) * sl.t_q * num_q_heads
+                                 : static_cast<size_t>(plan.n_slots) * wfk::kUnitTileRows;
     p.part_o = static_cast<float*>(workspace);
     p.part_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) +
                                           align256(rows * D * sizeof(float)));
@@ -1945,21 +2030,7 @@ int wf_attn_forward_fp8_block(const void* q, int num_q_heads,
     if (rc || plan.splits == 1) return rc;
     return D == 128 ? launch_join<128>(p, s) : launch_join<64>(p, s);
   }
-  rc = D == 128 ? launch_fp8_blocks<128>(p, sl, plan, s) : launch_fp8_blocks<64>(p, sl, plan, s);
-  if (rc || plan.splits == 1) return rc;
-  if (static_cast<int64_t>(sl.t_q) * num_q_heads <= kJoinRows)
-    return D == 128 ? launch_join<128>(p, s) : launch_join<64>(p, s);
-  const int64_t threads = static_cast<int64_t>(sl.t_q) * num_q_heads * 32;
-  const unsigned blocks =
-      static_cast<unsigned>((threads + wfk::kCombineThreads - 1) / wfk::kCombineThreads);
-  const wfk::CombinePlan cp{plan.splits, 0, 1, num_q_heads, sl.t_q};
-  if (D == 128)
-    wfk::wf_combine_kernel<128><<<blocks, wfk::kCombineThreads, 0, s>>>(
-        p.part_o, p.part_lse, cp, sl.t_q, num_q_heads, p.out, p.lse);
-  else
-    wfk::wf_combine_kernel<64><<<blocks, wfk::kCombineThreads, 0, s>>>(
-        p.part_o, p.part_lse, cp, sl.t_q, num_q_heads, p.out, p.lse);
-  return cudaGetLastError() == cudaSuccess ? WF_OK : WF_ERR_CUDA;
+  return D == 128 ? launch_fp8_blocks<128>(p, plan, s) : launch_fp8_blocks<64>(p, plan, s);
 }
 
 }  // extern "C"

@@ -580,8 +580,10 @@ int wf_kv_append_fp8_block(const wf_kv_pool_fp8_block_t* pool, int layer, int ch
  *                   values the cache stands for.  fp32 statistics and accumulation; weights are
  *                   rounded to 11 bits or more before P.V.
  *   lse_or_null     device fp32 [num_q_heads][rows] (optional).
- *   splits          S >= 1: every row's keys in S parts (at most 256), joined by a second launch; 0:
- *                   the library chooses.
+ *   splits          1: no row's keys are cut (no workspace).  0: the library cuts them so that the
+ *                   SMs are filled, and joins the parts in a second launch.  S > 1: with up to 32
+ *                   packed rows (rows x query heads of a K/V head) in every segment, S parts (at
+ *                   most 256); with more, as 0.
  *   workspace       device memory, 16-byte aligned, wf_attn_fp8_block_workspace_size bytes for the
  *                   same arguments; may be null when that is 0.  Not shared by calls, or captured
  *                   graphs, that may run at the same time.

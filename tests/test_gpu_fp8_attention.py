@@ -4,6 +4,13 @@ Tolerance.  Weights are rounded to 11 bits before P.V and the sum is not: 2^-11 
 and as much again for the fp32 steps around them.  A logit's fp32 sums are off by at most 2^-19 of
 L = scale sum |q| |k| (128 terms, and the scaling steps), which moves every weight by that much,
 twice (numerator and sum).  The output is rounded to bf16 once: 2^-8 of it.
+
+Under f16's normal range the rounding is absolute.  A weight is held as p 2^13 against a reference no
+larger than the maximum (so the sum is at least 1): half a step of 2^-24 is 2^-38 of it, a key's share
+of the output is off by at most 2^-38 |v|.  Where weights carry the value scale, p 2^13 2^(e - E), the
+half step is 2^-38 2^E in units of codes up to 448, and the largest value is at least 224 2^E: 2^-37 of
+the largest value.  Values held as f16 of code 2^(e - E + 7) are off by at most 2^-25 2^(E - 7), under
+2^-39 of the largest.  Together at most 2^-36 of the largest value for every key a row sees: FLOOR.
 """
 import numpy as np
 import pytest
@@ -16,6 +23,8 @@ from oracle import cache as oc
 from cache_util import BF16_HALF, bf16_rows
 
 pytestmark = pytest.mark.gpu
+
+FLOOR = 2.0 ** -36
 
 
 def make_cache(N, Hk, D, ps, seed, extra_pages=1, k_scale=1.0, v_scale=1.0):
@@ -50,7 +59,9 @@ def check(out, lse, q, vals, rows_end, kv_end, scale):
     k, group = vals[0], q.shape[1] // vals[0].shape[1]
     L = max((np.abs(qd[:, h]) @ np.abs(k[:, h // group]).T).max() * scale
             for h in range(q.shape[1])) if k.shape[0] and q.shape[0] else 0.0
-    tol = BF16_HALF * np.abs(want) + A * (2.0 ** -10 + 2.0 ** -18 * L) + 1e-38
+    seen = np.repeat(kv_end, np.diff([0] + list(rows_end)))[:, None, None]
+    top = np.abs(vals[1]).max(axis=(0, 2), initial=0.0).repeat(group)[None, :, None]
+    tol = BF16_HALF * np.abs(want) + A * (2.0 ** -10 + 2.0 ** -18 * L) + FLOOR * seen * top + 1e-38
     got = out.double().cpu().numpy()
     assert np.isfinite(got).all()
     worst = (np.abs(got - want) / tol).max()
@@ -79,6 +90,10 @@ CASES = [
     ([127, 255, 300, 557], [100, 1500, 257, 2049], 3, 3, 128, 64),
     ([600], [1111], 4, 2, 64, 16),
     ([256], [128], 8, 1, 128, 128),
+    # more row blocks than SMs: whole ones, shares that cut units, blocks without keys, odd halves
+    ([130, 700, 1500], [0, 300, 129], 40, 40, 64, 16),
+    ([1100, 4000], [1000, 700], 12, 12, 128, 64),
+    ([40, 700, 1300], [3000, 1, 515], 28, 7, 64, 32),
 ]
 
 
