@@ -99,7 +99,8 @@ struct AttnFp8Params {
   const int* page_table;
   __nv_bfloat16* out;
   float* lse;
-  float* part_o;                     // [slots][256 packed rows][D], a slot for each part of a cut unit
+  float* part_o;                     // [slots][D / 4][256 packed rows][4], a slot for each part of a
+                                     // cut unit: a thread's row is one of 256, so writes run along rows
   float* part_lse;                   // [slots][256]
   int* status;
   unsigned* grid_abort;
@@ -488,10 +489,12 @@ __global__ void __launch_bounds__(kFp8AttnThreads, 1)
             for (int i = 0; i < 32; ++i) r[i] = 0u;
           }
           if (live && part) {
-            float4* dst = reinterpret_cast<float4*>(p.part_o + prow * D + 32 * c);
+            float4* dst = reinterpret_cast<float4*>(p.part_o) +
+                          (static_cast<int64_t>(pc.slot) * (D / 4) + 8 * c) * kUnitTileRows +
+                          q * kBM + row;
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-              dst[i] = make_float4(
+              dst[i * kUnitTileRows] = make_float4(
                   __uint_as_float(r[4 * i]) * inv, __uint_as_float(r[4 * i + 1]) * inv,
                   __uint_as_float(r[4 * i + 2]) * inv, __uint_as_float(r[4 * i + 3]) * inv);
           } else if (live) {
@@ -585,6 +588,12 @@ __global__ void __launch_bounds__(kFp8AttnThreads, 1)
         auto exponent = [&](int tok) -> int {              // value scale of a token's block, biased
           return __ldg(p.v_scale + static_cast<int64_t>(fp8_row(p, tok) / 16) * p.Hk + pc.head);
         };
+        // exponent of this thread's row of a tile, looked up a tile ahead; -1: nothing to see there
+        auto row_exponent = [&](int t) -> int {
+          const int tok = (pc.kb + t) * BN + key / 16 * 16;
+          return t >= nk || tok >= pc.n_max ? -1 : exponent(tok);
+        };
+        int e_next = row_exponent(0);
         // the largest value exponent of this piece's keys
         int emax = 0;
 #pragma unroll 1
@@ -605,19 +614,14 @@ __global__ void __launch_bounds__(kFp8AttnThreads, 1)
           mbar_arrive(bar(L::B_EM + piece % L::NE));
         }
         ++piece;
-        auto factor = [&](int t) -> uint32_t {             // 2^(e_v - E + 7) as two f16
-          const int tok = (pc.kb + t) * BN + key / 16 * 16;
-          if (t >= nk || tok >= pc.n_max) return 0u;
-          const int e = exponent(tok) - 127 - emax + 7;
-          const uint32_t h = e >= -14 ? static_cast<uint32_t>(e + 15) << 10
-                             : e >= -24 ? 1u << (e + 24) : 0u;
-          return h | (h << 16);
-        };
-        uint32_t f_next = factor(0);
 #pragma unroll 1
         for (int j = 0; j < nk; ++j, ++it) {
-          const uint32_t f = f_next;
-          f_next = factor(j + 1);
+          // 2^(e_v - E + 7) as two f16, 0 below their range
+          const int e = e_next - 127 - emax + 7;
+          uint32_t f = e_next < 0 ? 0u : e >= -14 ? static_cast<uint32_t>(e + 15) << 10
+                       : e >= -24 ? 1u << (e + 24) : 0u;
+          f |= f << 16;
+          e_next = row_exponent(j + 1);
           const int cs = it % NC, vs = it % NV;
           ok = fp8_wait(bar(L::B_CF + cs), (it / NC) & 1, cta_abort) &&
                fp8_wait(bar(L::B_VE + vs), ((it / NV) & 1) ^ 1, cta_abort);
@@ -721,8 +725,9 @@ __global__ void __launch_bounds__(kFp8AttnThreads, 1)
   }
 }
 
-// Joins the pieces of the units that were cut: out = sum_s exp(lse_s - lse) O_s.  One warp per packed
-// row; grid (cut units, row groups).  The parts of a cut unit lie in consecutive slots.
+// Joins the pieces of the units that were cut: out = sum_s exp(lse_s - lse) O_s.  A block takes
+// kPieceJoinRows packed rows of a cut unit, a thread 4 channels of a row, rows fastest (the parts lie
+// that way).  The parts of a cut unit lie in consecutive slots.
 struct Fp8JoinParams {
   Fp8Units units;
   const float* part_o;
@@ -735,53 +740,54 @@ struct Fp8JoinParams {
   int parts[kFp8MaxCtas];
 };
 
-constexpr int kPieceJoinThreads = 256;
+constexpr int kPieceJoinRows = 8;
 
 template <int D>
-__global__ void __launch_bounds__(kPieceJoinThreads)
+__global__ void __launch_bounds__(kPieceJoinRows * D / 4)
     wf_piece_join_kernel(const __grid_constant__ Fp8JoinParams p) {
-  constexpr int PER = D / 32;
-  const int lane = threadIdx.x & 31;
+  constexpr int R = kPieceJoinRows, THREADS = R * D / 4;
+  __shared__ float wt[kFp8MaxCtas][R];       // log-sum-exps of every part and row
+  const int parts = p.parts[blockIdx.x];
+  const int64_t slot0 = p.slot[blockIdx.x];
+  const int tr = threadIdx.x % R, c = threadIdx.x / R;
+  const int r0 = static_cast<int>(blockIdx.y) * R;
   const UnitAt at = unit_at(p.units, p.unit[blockIdx.x]);
-  const int r = static_cast<int>(blockIdx.y) * (kPieceJoinThreads / 32) + (threadIdx.x >> 5);
-  const int m = at.m0 + r;
-  if (m >= p.units.seg_rows[at.seg] * p.units.group) return;
-  const int slot0 = p.slot[blockIdx.x], parts = p.parts[blockIdx.x];
-  const auto prow = [&](int s) -> int64_t {
-    return static_cast<int64_t>(slot0 + s) * kUnitTileRows + r;
-  };
+  const int m = at.m0 + r0 + tr;
+  if (at.m0 + r0 >= p.units.seg_rows[at.seg] * p.units.group) return;     // the whole block
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  for (int i = threadIdx.x; i < parts * R; i += THREADS)
+    wt[i / R][i % R] = p.part_lse[(slot0 + i / R) * kUnitTileRows + r0 + i % R];
+  const float4* o = reinterpret_cast<const float4*>(p.part_o) +
+                    (slot0 * (D / 4) + c) * kUnitTileRows + r0 + tr;
+  __syncthreads();
+  if (m >= p.units.seg_rows[at.seg] * p.units.group) return;
   float top = -INFINITY;
-  for (int s = lane; s < parts; s += 32) top = fmaxf(top, p.part_lse[prow(s)]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  for (int s = 0; s < parts; ++s) top = fmaxf(top, wt[s][tr]);
   const float ref = top == -INFINITY ? 0.f : top;
-  float total = 0.f, acc[PER];
+  float total = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s0 = 0; s0 < parts; s0 += 8) {    // eight parts' values in flight
+    float4 x[8];
 #pragma unroll
-  for (int c = 0; c < PER; ++c) acc[c] = 0.f;
-#pragma unroll 4
-  for (int s = 0; s < parts; ++s) {
-    const float wt = expf(p.part_lse[prow(s)] - ref);
-    const float* src = p.part_o + prow(s) * D + lane * PER;
-    float x[PER];
-    if (PER == 4) {
-      const float4 v = *reinterpret_cast<const float4*>(src);
-      x[0] = v.x, x[1] = v.y, x[PER - 2] = v.z, x[PER - 1] = v.w;
-    } else {
-      const float2 v = *reinterpret_cast<const float2*>(src);
-      x[0] = v.x, x[1] = v.y;
+    for (int i = 0; i < 8; ++i)
+      if (s0 + i < parts) x[i] = o[static_cast<int64_t>(s0 + i) * (D / 4) * kUnitTileRows];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (s0 + i >= parts) break;
+      const float w = expf(wt[s0 + i][tr] - ref);
+      total += w;
+      acc.x = fmaf(w, x[i].x, acc.x);
+      acc.y = fmaf(w, x[i].y, acc.y);
+      acc.z = fmaf(w, x[i].z, acc.z);
+      acc.w = fmaf(w, x[i].w, acc.w);
     }
-    total += wt;
-#pragma unroll
-    for (int c = 0; c < PER; ++c) acc[c] = fmaf(wt, x[c], acc[c]);
   }
   const float inv = total == 0.f ? 0.f : 1.f / total;
   const int64_t row = p.units.seg_row0[at.seg] + m / p.units.group;
   const int h = at.head * p.units.group + m % p.units.group;
-  uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + (row * p.Hq + h) * D + lane * PER);
-#pragma unroll
-  for (int c = 0; c < PER / 2; ++c) dst[c] = pack_bf16x2(acc[2 * c] * inv, acc[2 * c + 1] * inv);
-  if (lane == 0 && p.lse != nullptr)
+  *reinterpret_cast<uint2*>(p.out + (row * p.Hq + h) * D + 4 * c) =
+      make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+  if (c == 0 && p.lse != nullptr)
     p.lse[static_cast<int64_t>(h) * p.T_q + row] = total == 0.f ? -INFINITY : ref + logf(total);
 }
 

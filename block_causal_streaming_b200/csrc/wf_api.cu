@@ -1687,6 +1687,11 @@ struct Fp8Plan {
 // 32 rows 18 / 20, 64 rows 23 / 21.
 constexpr int kFewRows = 32;
 
+// What beginning another piece costs a CTA, in key tiles: Q's rows, a last tile's output and an empty
+// pipeline in between.  Measured, 0 / 4 / 8 / 16: 128 rows, 37 440 keys x 12 heads 75 / 60 / 57 / 62
+// us; 512 rows 128 / 114 / 113 / 117; 4680 rows 863 / 857 / 854 / 866.
+constexpr int kPieceCost = 8;
+
 // Spreads the key tiles of the row blocks over `ctas` CTAs (see the kernel): `n_whole` units go out
 // whole, unit k ctas + i to CTA i; the tiles of the others fill the CTAs up to one level, in unit
 // order.  Units of unequal length can leave whole turns uneven by more than the rest can fill: turns
@@ -1718,45 +1723,50 @@ void fp8_shares(Fp8Plan* pl, int num_sms) {
     }
   }
   pl->n_whole = turns * G;
-  // least level X with sum max(0, X - load) >= rest
-  int64_t level = 0, above = most + rest;
-  while (level < above) {
+  // Gives the rest out in unit order, each CTA up to `level`, a piece counting its tiles and
+  // kPieceCost; true when nothing is left over.
+  const auto give = [&](int64_t level, bool write) {
+    int unit = pl->n_whole, at = 0;
+    for (int i = 0; i < G; ++i) {
+      int64_t room = level - load[static_cast<size_t>(i)], take = 0;
+      if (write) {
+        pl->share_unit[i] = unit;
+        pl->share_tile[i] = at;
+        pl->share_slot[i] = pl->n_slots;
+      }
+      while (unit < pl->n_units && (take == 0 ? room > 0 : room > kPieceCost)) {
+        if (take > 0) room -= kPieceCost;          // (the first piece's cost is everyone's)
+        const int n = len[static_cast<size_t>(unit)];
+        const int piece = static_cast<int>(std::min<int64_t>(n - at, room));
+        if (write && piece < n) {                  // part of a unit
+          if (at == 0) {
+            pl->cut_unit[pl->n_cut] = unit;
+            pl->cut_slot[pl->n_cut] = pl->n_slots;
+            pl->cut_parts[pl->n_cut++] = 1;
+          } else {
+            ++pl->cut_parts[pl->n_cut - 1];
+          }
+          ++pl->n_slots;
+        }
+        room -= piece;
+        take += piece;
+        at += piece;
+        if (at == n) {
+          ++unit;
+          at = 0;
+        }
+      }
+      if (write) pl->share_tiles[i] = static_cast<int>(take);
+    }
+    return unit == pl->n_units;
+  };
+  int64_t level = 0, above = most + rest + kPieceCost * (pl->n_units - pl->n_whole);
+  while (level < above) {                          // the least level that does
     const int64_t x = (level + above) / 2;
-    int64_t room = 0;
-    for (int64_t l : load) room += std::max<int64_t>(0, x - l);
-    if (room >= rest) above = x;
+    if (give(x, false)) above = x;
     else level = x + 1;
   }
-  int unit = pl->n_whole, at = 0;
-  for (int i = 0; i < G; ++i) {
-    int64_t room = std::max<int64_t>(0, level - load[static_cast<size_t>(i)]);
-    pl->share_unit[i] = unit;
-    pl->share_tile[i] = at;
-    pl->share_slot[i] = pl->n_slots;
-    int64_t take = 0;
-    while (room > 0 && unit < pl->n_units) {
-      const int n = len[static_cast<size_t>(unit)];
-      const int piece = static_cast<int>(std::min<int64_t>(n - at, room));
-      if (piece < n) {                             // part of a unit
-        if (at == 0) {
-          pl->cut_unit[pl->n_cut] = unit;
-          pl->cut_slot[pl->n_cut] = pl->n_slots;
-          pl->cut_parts[pl->n_cut++] = 1;
-        } else {
-          ++pl->cut_parts[pl->n_cut - 1];
-        }
-        ++pl->n_slots;
-      }
-      room -= piece;
-      take += piece;
-      at += piece;
-      if (at == n) {
-        ++unit;
-        at = 0;
-      }
-    }
-    pl->share_tiles[i] = static_cast<int>(take);
-  }
+  give(level, true);
 }
 
 int fp8_plan(const SegmentList& sl, int Hq, int Hk, int splits, int num_sms, Fp8Plan* plan) {
@@ -1919,10 +1929,10 @@ int launch_fp8_blocks(const wfk::AttnFewParams& a, const Fp8Plan& plan, cudaStre
   std::memcpy(j.unit, plan.cut_unit, sizeof(int) * plan.n_cut);
   std::memcpy(j.slot, plan.cut_slot, sizeof(int) * plan.n_cut);
   std::memcpy(j.parts, plan.cut_parts, sizeof(int) * plan.n_cut);
-  const int rows = wfk::kPieceJoinThreads / 32;
   return launch_early(wfk::wf_piece_join_kernel<D>,
-                      dim3(static_cast<unsigned>(plan.n_cut), wfk::kUnitTileRows / rows),
-                      wfk::kPieceJoinThreads, s, j);
+                      dim3(static_cast<unsigned>(plan.n_cut),
+                           wfk::kUnitTileRows / wfk::kPieceJoinRows),
+                      wfk::kPieceJoinRows * D / 4, s, j);
 }
 
 }  // namespace
