@@ -608,7 +608,7 @@ __global__ void wf_selftest_timeout_kernel(int* status, unsigned* grid_abort, un
 
 extern "C" {
 
-int wf_version(void) { return 100; }
+int wf_version(void) { return 200; }
 
 const char* wf_strerror(int code) {
   switch (code) {

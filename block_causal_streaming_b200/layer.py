@@ -47,6 +47,49 @@ class PagedPoolFp8:
         return self.k_codes, self.v_codes, self.k_scale, self.v_scale
 
 
+class PagedPoolFp8Block:
+    """FP8 cache that attention reads in place (wf_kv_pool_fp8_block_t): e4m3 codes uint8
+    [num_pages, page_size, H, D] and e8m0 scales uint8 [num_pages, page_size / 16, H] (a byte b
+    stands for 2^(b - 127)) for K and for V, zeroed.  Filled by wf_kv_append_fp8_block, read by
+    wf_attn_forward_fp8_block."""
+
+    def __init__(self, num_pages: int, page_size: int, heads: int, head_dim: int,
+                 device="cuda"):
+        if page_size < 16 or page_size % 16:
+            raise ValueError(f"page_size: a positive multiple of 16, got {page_size}")
+        shape = (num_pages, page_size, heads, head_dim)
+        blocks = (num_pages, page_size // 16, heads)
+        self.k_codes = torch.zeros(shape, dtype=torch.uint8, device=device)
+        self.v_codes = torch.zeros(shape, dtype=torch.uint8, device=device)
+        self.k_scale = torch.zeros(blocks, dtype=torch.uint8, device=device)
+        self.v_scale = torch.zeros(blocks, dtype=torch.uint8, device=device)
+        self.num_pages, self.page_size, self.heads, self.head_dim = shape
+
+    @property
+    def tensors(self):
+        return self.k_codes, self.v_codes, self.k_scale, self.v_scale
+
+
+def rotation_table(rows: int, axis_pairs: Sequence[int], base: float = 10000.0,
+                   device="cuda") -> torch.Tensor:
+    """The table of a :class:`NormRope`: fp32 [rows, pairs, 2], cos and sin of position times
+    base^(-i / n) for pair i of an axis with n pairs, computed in 64 bits (far positions have
+    angles that 32 bits cannot hold)."""
+    freq = torch.cat([base ** (-torch.arange(n, dtype=torch.float64) / max(n, 1))
+                      for n in axis_pairs])
+    ang = torch.arange(rows, dtype=torch.float64)[:, None] * freq
+    return torch.stack((ang.cos(), ang.sin()), -1).float().to(device).contiguous()
+
+
+def video_positions(first_token: int, tokens: int, rows: int, cols: int,
+                    device="cuda") -> torch.Tensor:
+    """int32 [tokens, 3]: frame, row and column of ``tokens`` tokens of a video whose frames are
+    rows x cols patches, from ``first_token`` on."""
+    t = torch.arange(first_token, first_token + tokens)
+    pos = torch.stack((t // (rows * cols), t // cols % rows, t % cols), 1)
+    return pos.to(torch.int32).to(device).contiguous()
+
+
 class QkI8Buffers:
     """The device buffers of the INT8 attention tier for one wavefront shape (see
     ``wf_qk_quantize_i8``): int8 Q and K' codes, their per-128-row scales, the key mean and its
@@ -117,6 +160,14 @@ class WavefrontLayer:
             a, b = self.chunk_offsets[c], self.chunk_offsets[c + 1]
             self.append(c, k_all[a:b], v_all[a:b], stream)
 
+    def append_rope(self, chunk_begin: int, chunk_end: int, k: torch.Tensor, v: torch.Tensor, rule,
+                    positions=None, k_weight=None, stream=None) -> None:
+        """Append chunks [chunk_begin, chunk_end), keys normed and rotated on the way (``rule``: a
+        :class:`NormRope`); ``k``, ``v``: their rows, [L, H, D], slices of a projection's output
+        as they are."""
+        _abi.kv_append_rope(self.pool.k, self.pool.v, self.layer, chunk_begin, chunk_end, k, v,
+                            self.page_tables, self.desc, rule, positions, k_weight, stream)
+
     def forward_i8(self, q: torch.Tensor, out: torch.Tensor, qk: "QkI8Buffers",
                    scale: Optional[float] = None, lse: Optional[torch.Tensor] = None,
                    stream=None) -> None:
@@ -165,3 +216,54 @@ class WavefrontLayer:
             ws = self._workspace
         _abi.attn_forward_split(q, self.pool.k, self.pool.v, self.page_tables[self.layer],
                                 self.desc, scale, out, splits, ws, lse, stream)
+
+
+class Fp8BlockLayer:
+    """One layer of a wavefront over an FP8 cache that attention reads in place.
+
+    ``pool``: a :class:`PagedPoolFp8Block`, which several layers may share; the other arguments as
+    for :class:`WavefrontLayer`.  Query heads may be a multiple of the pool's heads.
+    """
+
+    def __init__(self, pool: PagedPoolFp8Block, page_tables: torch.Tensor, layer: int,
+                 chunk_offsets: Sequence[int], chunk_stage: Sequence[int], num_ctx_chunks: int):
+        self.pool = pool
+        self.page_tables = page_tables
+        self.layer = int(layer)
+        self.desc = _abi.WavefrontDesc(chunk_offsets, chunk_stage, num_ctx_chunks,
+                                       page_tables.shape[1])
+        off = self.chunk_offsets = list(chunk_offsets)
+        first = off[num_ctx_chunks]
+        self.segments = _abi.Segments([e - first for e in off[num_ctx_chunks + 1:]],
+                                      off[num_ctx_chunks + 1:], off[-1], page_tables.shape[1])
+        self._workspace: Optional[torch.Tensor] = None
+
+    def append(self, chunk_begin: int, chunk_end: int, k: torch.Tensor, v: torch.Tensor, rule=None,
+               positions=None, k_weight=None, stream=None) -> None:
+        """Append chunks [chunk_begin, chunk_end) (``k``, ``v``: their rows, [L, H, D] bf16), keys
+        normed and rotated on the way when ``rule`` is given."""
+        _abi.kv_append_fp8_block(*self.pool.tensors, self.layer, chunk_begin, chunk_end, k, v,
+                                 self.page_tables, self.desc, rule, positions, k_weight, stream)
+
+    def workspace_size(self, q_heads: int, segments=None, splits: int = 0) -> int:
+        return _abi.attn_fp8_block_workspace_size(segments or self.segments, q_heads,
+                                                  self.pool.heads, self.pool.head_dim, splits)
+
+    def forward(self, q: torch.Tensor, out: torch.Tensor, scale: Optional[float] = None,
+                lse: Optional[torch.Tensor] = None, splits: int = 0,
+                workspace: Optional[torch.Tensor] = None, segments=None, stream=None) -> None:
+        """Attention of ``q`` over this layer's cache: the wavefront's query chunks, each up to its
+        own end, or the rows of ``segments``.  Without ``workspace`` the layer allocates one and
+        reuses it; calls and captured graphs that may run at the same time need one each."""
+        if scale is None:
+            scale = 1.0 / math.sqrt(self.pool.head_dim)
+        seg = segments or self.segments
+        if workspace is None:
+            need = self.workspace_size(q.shape[1], seg, splits)
+            if need > 0:
+                if self._workspace is None or self._workspace.numel() < need or \
+                        self._workspace.device != q.device:
+                    self._workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+                workspace = self._workspace
+        _abi.attn_forward_fp8_block(q, *self.pool.tensors, self.page_tables[self.layer], seg, scale,
+                                    out, lse, splits, workspace, stream)

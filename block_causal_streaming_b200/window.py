@@ -181,17 +181,26 @@ class RollingCache:
     Each round, for every layer: :meth:`run_layer` appends the round's query chunks (store pass
     first, then the chunks in flight, in the order of :meth:`RollingWindow.view`).  It then runs
     attention for all of them in one launch and, once the ring is full, hands the store chunk into
-    the slot of the chunk that leaves.
+    the slot of the chunk that leaves.  ``fp8_block``: the K/V stay in an FP8 cache with one scale
+    for 16 tokens and head (:class:`layer.PagedPoolFp8Block`), which attention reads in place.
     """
 
     def __init__(self, window: RollingWindow, heads: int, head_dim: int, num_layers: int = 1,
                  device="cuda", page_tables: Optional[torch.Tensor] = None,
-                 fill: Optional[float] = None):
-        from .layer import PagedPool
+                 fill: Optional[float] = None, fp8_block: bool = False):
+        from .layer import PagedPool, PagedPoolFp8Block
         self.window = window
         self.num_layers = int(num_layers)
-        self.pool = PagedPool(window.pages * self.num_layers, window.page_size, heads, head_dim,
-                              device, fill=fill)
+        self.fp8_block = bool(fp8_block)
+        if self.fp8_block:
+            if fill is not None:
+                raise ValueError("an FP8 cache starts out zeroed: no fill")
+            self.pool = PagedPoolFp8Block(window.pages * self.num_layers, window.page_size, heads,
+                                          head_dim, device)
+        else:
+            self.pool = PagedPool(window.pages * self.num_layers, window.page_size, heads,
+                                  head_dim, device, fill=fill)
+        self._workspace: Optional[torch.Tensor] = None
         if page_tables is None:
             page_tables = torch.arange(window.pages * self.num_layers, dtype=torch.int32)
             page_tables = page_tables.view(self.num_layers, window.pages)
@@ -200,19 +209,27 @@ class RollingCache:
         self.page_tables = page_tables.to(device=device, dtype=torch.int32).contiguous()
 
     def layer_view(self, view: RoundView, layer: int):
-        from .layer import WavefrontLayer
-        return WavefrontLayer(self.pool, self.page_tables, layer, view.chunk_offsets,
+        from .layer import Fp8BlockLayer, WavefrontLayer
+        cls = Fp8BlockLayer if self.fp8_block else WavefrontLayer
+        return cls(self.pool, self.page_tables, layer, view.chunk_offsets,
                               view.chunk_stage, view.num_ctx_chunks)
 
     def run_layer(self, view: RoundView, layer: int, q: torch.Tensor, k: torch.Tensor,
                   v: torch.Tensor, out: torch.Tensor, scale: Optional[float] = None,
-                  lse: Optional[torch.Tensor] = None, stream=None) -> None:
+                  lse: Optional[torch.Tensor] = None, stream=None, rule=None, positions=None,
+                  k_weight=None) -> None:
         """One layer of round ``view.round``.  ``q``, ``k``, ``v``, ``out``: bf16 [T_q, H, D], the
-        rows of the round's query chunks in logical order (store pass, then in flight)."""
+        rows of the round's query chunks in logical order (store pass, then in flight).  With
+        ``rule`` (a :class:`NormRope`) the keys are normed and rotated on their way into the cache;
+        ``positions``: int32 [T_q, axes], of the same rows."""
         if view.t_q == 0:
             return
         lay = self.layer_view(view, layer)
         L = self.window.chunk_len
+        if self.fp8_block or rule is not None:
+            self._run_cache(view, layer, lay, q, k, v, out, scale, lse, stream, rule, positions,
+                            k_weight)
+            return
         if self.window.copy_free:
             self._run_segments(view, layer, lay, q, k, v, out, scale, lse, stream)
             return
@@ -223,6 +240,43 @@ class RollingCache:
             # the store chunk is the first query chunk; after this layer's attention the evicted
             # chunk is no longer read, so its slot takes the store chunk's clean K/V
             lay.append(view.store_to, k[:L], v[:L], stream)
+
+    def _run_cache(self, view: RoundView, layer: int, lay, q, k, v, out, scale, lse, stream, rule,
+                   positions, k_weight) -> None:
+        """A round with an FP8 cache or with keys that are normed and rotated on the way in."""
+        from . import _abi
+        L = self.window.chunk_len
+
+        def append(slot, i):
+            rows = slice(i * L, (i + 1) * L)
+            args = (slot, slot + 1, k[rows], v[rows], rule,
+                    None if positions is None else positions[rows], k_weight, stream)
+            if self.fp8_block:
+                lay.append(*args)
+            else:
+                lay.append_rope(*args)
+        slots = view.query_rows_slots if self.window.copy_free else view.query_slots
+        for i, slot in enumerate(slots):
+            append(slot, i)
+        seg = None
+        if self.window.copy_free:
+            rows_end, kv_end = view.segments()
+            seg = _abi.Segments(rows_end, kv_end, view.chunk_offsets[-1],
+                                self.page_tables.shape[1])
+        if self.fp8_block:
+            need = lay.workspace_size(q.shape[1], seg)
+            if need and (self._workspace is None or self._workspace.numel() < need):
+                self._workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+            lay.forward(q, out, scale, lse, 0, self._workspace if need else None, seg, stream)
+        elif seg is not None:
+            if scale is None:
+                scale = 1.0 / math.sqrt(self.pool.head_dim)
+            _abi.attn_forward_segments(q, self.pool.k, self.pool.v, self.page_tables[layer], seg,
+                                       scale, out, lse, 1, None, stream)
+        else:
+            lay.forward(q, out, scale=scale, lse=lse, stream=stream)
+        if view.store_to is not None:
+            append(view.store_to, 0)              # the store chunk takes the evicted chunk's slot
 
     def _run_segments(self, view: RoundView, layer: int, lay, q, k, v, out, scale, lse,
                       stream) -> None:
