@@ -211,8 +211,11 @@ __global__ void __launch_bounds__(kFewThreads, FewSmem<D, NT>::CTAS)
   const int lo = static_cast<int>(static_cast<int64_t>(split) * blocks / p.splits) + warp;
   const int hi = static_cast<int>(static_cast<int64_t>(split + 1) * blocks / p.splits);
   const int nk = hi > lo ? (hi - lo + kFewWarps - 1) / kFewWarps : 0;
-  if (threadIdx.x == 0)
+  if (threadIdx.x == 0) {
     *cta_abort = (*reinterpret_cast<volatile unsigned*>(p.grid_abort) == p.launch_id) ? 1 : 0;
+    // (a captured launch keeps its id: a replay after a wait ran out says so again)
+    if (*cta_abort) atomicCAS(p.status, 0, 6 /* WF_ERR_TIMEOUT */);
+  }
   if (lane == 0) {
     for (int i = 0; i < NS; ++i) mbar_init(full(i), 1);
     mbar_init_fence();

@@ -283,6 +283,8 @@ __global__ void __launch_bounds__(kFp8AttnThreads, 1)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the join waits by itself
   if (threadIdx.x == 0) {
     *cta_abort = (*reinterpret_cast<volatile unsigned*>(p.grid_abort) == p.launch_id) ? 1 : 0;
+    // (a captured launch keeps its id: a replay after a wait ran out says so again)
+    if (*cta_abort) atomicCAS(p.status, 0, 6 /* WF_ERR_TIMEOUT */);
     for (int i = 0; i < L::NBAR; ++i) {
       uint32_t count = 1;
       if (i < L::B_KF) count = 128u;
@@ -342,8 +344,9 @@ __global__ void __launch_bounds__(kFp8AttnThreads, 1)
           mw = __vmaxu2(mw, x[c].z & 0x7FFF7FFFu);
           mw = __vmaxu2(mw, x[c].w & 0x7FFF7FFFu);
         }
-        const int e = scale_exponent(__uint_as_float(max(mw & 0xFFFFu, mw >> 16) << 16));
-        const float f = exp2_int(-e);
+        const uint32_t top = max(mw & 0xFFFFu, mw >> 16);   // an infinite value makes its row NaN
+        const int e = scale_exponent(__uint_as_float(top << 16));
+        const float f = top < 0x7F80u ? exp2_int(-e) : __uint_as_float(0x7FFFFFFFu);
         sl2 = p.sl2 * exp2_int(e);
         const uint32_t hi_t = base + L::Q_OFF + 2 * q * L::QTERM, lo_t = hi_t + L::QTERM;
 #pragma unroll

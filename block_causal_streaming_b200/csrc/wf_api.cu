@@ -1692,35 +1692,40 @@ constexpr int kFewRows = 32;
 // us; 512 rows 128 / 114 / 113 / 117; 4680 rows 863 / 857 / 854 / 866.
 constexpr int kPieceCost = 8;
 
+// Units a CTA from which on none is cut: whole ones are then even enough.
+constexpr int kWholeUnits = 48;
+
 // Spreads the key tiles of the row blocks over `ctas` CTAs (see the kernel): `n_whole` units go out
 // whole, unit k ctas + i to CTA i; the tiles of the others fill the CTAs up to one level, in unit
 // order.  Units of unequal length can leave whole turns uneven by more than the rest can fill: turns
 // are given up to the rest until the fullest CTA is within 2 % of an even share.
 void fp8_shares(Fp8Plan* pl, int num_sms) {
   const wfk::Fp8Units& u = pl->units;
-  const auto tiles = [&](int unit) {
-    return (u.seg_kv[wfk::unit_at(u, unit).seg] + wfk::kBN - 1) / wfk::kBN;
-  };
+  const int cap = std::min(num_sms, wfk::kFp8MaxCtas);
+  pl->ctas = cap;
+  pl->n_whole = pl->n_units;
+  for (int i = 0; i < cap; ++i)
+    pl->share_unit[i] = pl->share_tile[i] = pl->share_tiles[i] = pl->share_slot[i] = 0;
+  if (pl->n_units >= kWholeUnits * cap) return;
+  int len[kWholeUnits * wfk::kFp8MaxCtas];         // key tiles of every unit
   int64_t total = 0;
-  std::vector<int> len(static_cast<size_t>(pl->n_units));
-  for (int i = 0; i < pl->n_units; ++i) total += len[static_cast<size_t>(i)] = tiles(i);
-  const int G = static_cast<int>(std::min<int64_t>(
-      std::min(num_sms, wfk::kFp8MaxCtas), std::max<int64_t>({total, pl->n_blank, 1})));
-  pl->ctas = G;
-  std::vector<int64_t> load(static_cast<size_t>(G), 0);
-  int turns = pl->n_units / G;
-  int64_t rest = total, most = 0;
-  for (int i = 0; i < turns * G; ++i) {
-    load[static_cast<size_t>(i % G)] += len[static_cast<size_t>(i)];
-    rest -= len[static_cast<size_t>(i)];
+  for (int i = 0; i < pl->n_units; ++i) {
+    len[i] = (u.seg_kv[wfk::unit_at(u, i).seg] + wfk::kBN - 1) / wfk::kBN;
+    total += len[i];
   }
+  // from here on in cost: a piece's tiles and kPieceCost
+  const int G = static_cast<int>(
+      std::min<int64_t>(cap, std::max<int64_t>({total, pl->n_blank, 1})));
+  pl->ctas = G;
+  total += static_cast<int64_t>(kPieceCost) * pl->n_units;
+  int64_t load[wfk::kFp8MaxCtas] = {};
+  int turns = pl->n_units / G;
+  int64_t most = 0;
+  for (int i = 0; i < turns * G; ++i) load[i % G] += len[i] + kPieceCost;
   for (;; --turns) {
-    most = *std::max_element(load.begin(), load.end());
+    most = *std::max_element(load, load + G);
     if (turns == 0 || most * G <= total + total / 50) break;
-    for (int i = (turns - 1) * G; i < turns * G; ++i) {
-      load[static_cast<size_t>(i % G)] -= len[static_cast<size_t>(i)];
-      rest += len[static_cast<size_t>(i)];
-    }
+    for (int i = (turns - 1) * G; i < turns * G; ++i) load[i % G] -= len[i] + kPieceCost;
   }
   pl->n_whole = turns * G;
   // Gives the rest out in unit order, each CTA up to `level`, a piece counting its tiles and
@@ -1728,15 +1733,15 @@ void fp8_shares(Fp8Plan* pl, int num_sms) {
   const auto give = [&](int64_t level, bool write) {
     int unit = pl->n_whole, at = 0;
     for (int i = 0; i < G; ++i) {
-      int64_t room = level - load[static_cast<size_t>(i)], take = 0;
+      int64_t room = level - load[i], take = 0;
       if (write) {
         pl->share_unit[i] = unit;
         pl->share_tile[i] = at;
         pl->share_slot[i] = pl->n_slots;
       }
-      while (unit < pl->n_units && (take == 0 ? room > 0 : room > kPieceCost)) {
-        if (take > 0) room -= kPieceCost;          // (the first piece's cost is everyone's)
-        const int n = len[static_cast<size_t>(unit)];
+      while (unit < pl->n_units && room > kPieceCost) {
+        room -= kPieceCost;
+        const int n = len[unit];
         const int piece = static_cast<int>(std::min<int64_t>(n - at, room));
         if (write && piece < n) {                  // part of a unit
           if (at == 0) {
@@ -1760,7 +1765,7 @@ void fp8_shares(Fp8Plan* pl, int num_sms) {
     }
     return unit == pl->n_units;
   };
-  int64_t level = 0, above = most + rest + kPieceCost * (pl->n_units - pl->n_whole);
+  int64_t level = 0, above = most + total + kPieceCost + 1;
   while (level < above) {                          // the least level that does
     const int64_t x = (level + above) / 2;
     if (give(x, false)) above = x;

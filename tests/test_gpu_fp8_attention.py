@@ -207,3 +207,51 @@ def test_bad_pages_are_recorded(rows):
     assert check_status() == WF_OK                          # the bad page is past the limit
     run(q, cache, pt, Segments([rows], [49], 100, pt.numel()), 0.1)
     assert check_status() == WF_ERR_PAGE_OOB and check_status() == WF_OK
+
+
+@pytest.mark.parametrize("rows", [3, 130])
+def test_a_query_that_is_not_finite_stays_in_its_row(rows):
+    N, H, D, ps = 300, 2, 64, 16
+    cache, pt, _ = make_cache(N, H, D, ps, 80)
+    q = bf16_rows(rows, H, D, 81).cuda()
+    seg = Segments([rows], [N], N, pt.numel())
+    base, base_lse = run(q, cache, pt, seg, 0.1)
+    q[1, 0, 3], q[2, 1, 5] = float("nan"), float("inf")
+    out, lse = run(q, cache, pt, seg, 0.1)
+    assert check_status() == WF_OK
+    bad = torch.zeros(rows, H, dtype=torch.bool, device="cuda")
+    bad[1, 0] = bad[2, 1] = True
+    assert out[bad].isnan().all() and torch.equal(out[~bad], base[~bad])
+    assert torch.equal(lse[~bad.t()], base_lse[~bad.t()]) and not lse[bad.t()].isfinite().any()
+
+
+def test_a_cache_past_2_gib():
+    """Pages whose codes (and bf16 pool values) lie past 2^31 bytes and values."""
+    from block_causal_streaming_b200 import NormRope, kv_append_rope
+    H, D, ps, N = 8, 128, 64, 300
+    pages = 2 ** 31 // (ps * H * D) + 40
+    row = torch.arange(pages - 5, pages).int().view(1, -1).cuda()
+    codes = [torch.zeros(pages, ps, H, D, dtype=torch.uint8, device="cuda") for _ in "kv"]
+    scale = [torch.zeros(pages, ps // 16, H, dtype=torch.uint8, device="cuda") for _ in "kv"]
+    k, v = bf16_rows(N, H, D, 90).cuda(), bf16_rows(N, H, D, 91).cuda()
+    wf = WavefrontDesc([0, N], [0], 0, 5)
+    kv_append_fp8_block(*codes, *scale, 0, 0, 1, k, v, row, wf)
+    tail = [c[-5:].clone() for c in codes] + [s[-5:].clone() for s in scale]
+    small = [torch.zeros(5, ps, H, D, dtype=torch.uint8, device="cuda") for _ in "kv"] + \
+        [torch.zeros(5, ps // 16, H, dtype=torch.uint8, device="cuda") for _ in "kv"]
+    at = torch.arange(5).int().cuda()
+    kv_append_fp8_block(*small, 0, 0, 1, k, v, at.view(1, -1), wf)
+    assert all(torch.equal(a, b) for a, b in zip(tail, small))
+    assert all(int(c[:-5].sum(dtype=torch.int64)) == 0 for c in codes)
+    for rows in (1, 150):
+        q = bf16_rows(rows, H, D, 92).cuda()
+        seg = Segments([rows], [N], N, 5)
+        a, la = run(q, codes + scale, row[0], seg, 0.1)
+        b, lb = run(q, small, at, seg, 0.1)
+        assert torch.equal(a, b) and torch.equal(la, lb)
+    del codes, scale
+    pools = [torch.zeros(pages, ps, H, D, dtype=torch.bfloat16, device="cuda") for _ in "kv"]
+    kv_append_rope(*pools, 0, 0, 1, k, v, row, wf, NormRope(None, norm=False))
+    assert torch.equal(pools[0][-5:].flatten(0, 1)[:N], k)
+    assert torch.equal(pools[1][-5:].flatten(0, 1)[:N], v)
+    assert not pools[0][:-5].any() and check_status() == WF_OK
