@@ -189,9 +189,6 @@ __global__ void __launch_bounds__(kFewThreads, FewSmem<D, NT>::CTAS)
   auto full = [&](int i) -> uint32_t { return base + L::BAR_OFF + 8u * (warp * NS + i); };
   const uint32_t ring = base + L::RING_OFF + warp * (NS * 2 * L::CTILE);
   volatile int* const cta_abort = reinterpret_cast<volatile int*>(few_smem + L::MISC_OFF);
-  // the join's blocks may take their places as soon as every CTA of this launch has its own; they
-  // wait for its results all the same
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const WaitCtx w8{cta_abort, p.grid_abort, p.status, p.launch_id, 6 /* WF_ERR_TIMEOUT */,
                    2000000000ull};
 
@@ -211,14 +208,16 @@ __global__ void __launch_bounds__(kFewThreads, FewSmem<D, NT>::CTAS)
   const int lo = static_cast<int>(static_cast<int64_t>(split) * blocks / p.splits) + warp;
   const int hi = static_cast<int>(static_cast<int64_t>(split + 1) * blocks / p.splits);
   const int nk = hi > lo ? (hi - lo + kFewWarps - 1) / kFewWarps : 0;
+  if (lane == 0) {
+    for (int i = 0; i < NS; ++i) mbar_init(full(i), 1);
+    mbar_init_fence();
+  }
+  wait_for_previous();
+  launch_next();
   if (threadIdx.x == 0) {
     *cta_abort = (*reinterpret_cast<volatile unsigned*>(p.grid_abort) == p.launch_id) ? 1 : 0;
     // (a captured launch keeps its id: a replay after a wait ran out says so again)
     if (*cta_abort) atomicCAS(p.status, 0, 6 /* WF_ERR_TIMEOUT */);
-  }
-  if (lane == 0) {
-    for (int i = 0; i < NS; ++i) mbar_init(full(i), 1);
-    mbar_init_fence();
   }
   // lane j % 32 looks up the pool row and the scales of block j, 32 blocks at a time
   int my_row = 0, my_ks = 127, my_vs = 127;
@@ -526,7 +525,8 @@ __global__ void __launch_bounds__(kJoinThreads)
   __shared__ float wt[kMaxJoin], red[kJoinThreads / 32], acc_s[kJoinThreads / 32][D];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
   const int row = static_cast<int>(blockIdx.x) / Hq, h = static_cast<int>(blockIdx.x) % Hq;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  wait_for_previous();
+  launch_next();
   const float ls = tid < splits
                        ? part_lse[(static_cast<int64_t>(tid) * Hq + h) * T_q + row] : -INFINITY;
   float top = ls;

@@ -280,11 +280,7 @@ __global__ void __launch_bounds__(kFp8AttnThreads, 1)
   auto bar = [&](int i) -> uint32_t { return base + L::BAR_OFF + 8u * static_cast<uint32_t>(i); };
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the join waits by itself
   if (threadIdx.x == 0) {
-    *cta_abort = (*reinterpret_cast<volatile unsigned*>(p.grid_abort) == p.launch_id) ? 1 : 0;
-    // (a captured launch keeps its id: a replay after a wait ran out says so again)
-    if (*cta_abort) atomicCAS(p.status, 0, 6 /* WF_ERR_TIMEOUT */);
     for (int i = 0; i < L::NBAR; ++i) {
       uint32_t count = 1;
       if (i < L::B_KF) count = 128u;
@@ -299,6 +295,13 @@ __global__ void __launch_bounds__(kFp8AttnThreads, 1)
   if (warp == 8) {
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
+  }
+  wait_for_previous();
+  launch_next();
+  if (threadIdx.x == 0) {
+    *cta_abort = (*reinterpret_cast<volatile unsigned*>(p.grid_abort) == p.launch_id) ? 1 : 0;
+    // (a captured launch keeps its id: a replay after a wait ran out says so again)
+    if (*cta_abort) atomicCAS(p.status, 0, 6 /* WF_ERR_TIMEOUT */);
   }
   tc_fence_before();
   __syncthreads();
@@ -757,7 +760,8 @@ __global__ void __launch_bounds__(kPieceJoinRows * D / 4)
   const UnitAt at = unit_at(p.units, p.unit[blockIdx.x]);
   const int m = at.m0 + r0 + tr;
   if (at.m0 + r0 >= p.units.seg_rows[at.seg] * p.units.group) return;     // the whole block
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  wait_for_previous();
+  launch_next();
   for (int i = threadIdx.x; i < parts * R; i += THREADS)
     wt[i / R][i % R] = p.part_lse[(slot0 + i / R) * kUnitTileRows + r0 + i % R];
   const float4* o = reinterpret_cast<const float4*>(p.part_o) +

@@ -98,6 +98,8 @@ __global__ void __launch_bounds__(kNormRopeThreads, kFp8AppendCtas)
   __shared__ float4 angles[kMode != kRopeNone ? kFp8BlockTokens * CSP : 1];
   __shared__ float stage_all[kMode == kRopeSplitPartial ? kNormRopeThreads * 16 : 1];
   __shared__ float tops[2][kFp8AppendPairs][2];
+  wait_for_previous();
+  launch_next();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   float* const stage = stage_all + (kMode == kRopeSplitPartial ? warp * 512 : 0);
   const int sub = lane % LPR;

@@ -269,6 +269,8 @@ __global__ void __launch_bounds__(kNormRopeThreads, kNormRopeCtas)
     wf_norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
   constexpr int LPR = D / 16, RPS = 32 / LPR, B = kNormRopeBatch;   // lanes per row, rows per step
   __shared__ float stage_all[kMode == kRopeSplitPartial ? kNormRopeThreads * 16 : 1];
+  wait_for_previous();
+  launch_next();
   const int lane = threadIdx.x & 31;
   float* const stage = stage_all + (kMode == kRopeSplitPartial ? (threadIdx.x >> 5) * 512 : 0);
   const int sub = lane % LPR, rsub = lane / LPR;

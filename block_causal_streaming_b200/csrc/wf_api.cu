@@ -1440,6 +1440,28 @@ int block_count(const DeviceState* d, int64_t items, int per_sm) {
   return static_cast<int>(std::min<int64_t>(blocks, static_cast<int64_t>(d->num_sms) * per_sm));
 }
 
+// A launch whose blocks may take their places while the kernel before it still runs; they begin with
+// wait_for_previous().
+template <typename... Args, typename... Given>
+int launch_early(void (*kernel)(Args...), dim3 grid, int threads, int smem, cudaStream_t s,
+                 const Given&... given) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = s;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, static_cast<Args>(given)...) != cudaSuccess) {
+    cudaGetLastError();
+    return WF_ERR_CUDA;
+  }
+  return WF_OK;
+}
+
 // Splits each token's rows into work items and launches.
 template <bool kAppend>
 int launch_norm_rope(wfk::NormRopeParams* p, wfk::RopeMode mode, int D, const DeviceState* d,
@@ -1453,20 +1475,20 @@ int launch_norm_rope(wfk::NormRopeParams* p, wfk::RopeMode mode, int D, const De
   p->items_per_token = (steps + p->chunk - 1) / p->chunk;
   const int blocks = block_count(d, static_cast<int64_t>(p->tokens) * p->items_per_token, 16);
   const int th = wfk::kNormRopeThreads;
-#define WF_LAUNCH(D_, M_) wfk::wf_norm_rope_kernel<D_, M_, kAppend><<<blocks, th, 0, s>>>(*p)
+#define WF_LAUNCH(D_, M_) \
+  return launch_early(wfk::wf_norm_rope_kernel<D_, M_, kAppend>, dim3(blocks), th, 0, s, *p)
   if (D == 128) {
     if (mode == wfk::kRopeNone) WF_LAUNCH(128, wfk::kRopeNone);
-    else if (mode == wfk::kRopeInterleaved) WF_LAUNCH(128, wfk::kRopeInterleaved);
-    else if (mode == wfk::kRopeSplit) WF_LAUNCH(128, wfk::kRopeSplit);
-    else WF_LAUNCH(128, wfk::kRopeSplitPartial);
+    if (mode == wfk::kRopeInterleaved) WF_LAUNCH(128, wfk::kRopeInterleaved);
+    if (mode == wfk::kRopeSplit) WF_LAUNCH(128, wfk::kRopeSplit);
+    WF_LAUNCH(128, wfk::kRopeSplitPartial);
   } else {
     if (mode == wfk::kRopeNone) WF_LAUNCH(64, wfk::kRopeNone);
-    else if (mode == wfk::kRopeInterleaved) WF_LAUNCH(64, wfk::kRopeInterleaved);
-    else if (mode == wfk::kRopeSplit) WF_LAUNCH(64, wfk::kRopeSplit);
-    else WF_LAUNCH(64, wfk::kRopeSplitPartial);
+    if (mode == wfk::kRopeInterleaved) WF_LAUNCH(64, wfk::kRopeInterleaved);
+    if (mode == wfk::kRopeSplit) WF_LAUNCH(64, wfk::kRopeSplit);
+    WF_LAUNCH(64, wfk::kRopeSplitPartial);
   }
 #undef WF_LAUNCH
-  return cudaGetLastError() == cudaSuccess ? WF_OK : WF_ERR_CUDA;
 }
 
 // The token range of chunks [chunk_begin, chunk_end) and the checks the two appends share, after
@@ -1615,20 +1637,20 @@ int wf_kv_append_fp8_block(const wf_kv_pool_fp8_block_t* pool, int layer, int ch
   const dim3 blocks(static_cast<unsigned>(nb), static_cast<unsigned>(runs));
   const int th = wfk::kNormRopeThreads;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-#define WF_LAUNCH(D_, M_) wfk::wf_fp8_block_append_kernel<D_, M_><<<blocks, th, 0, s>>>(p)
+#define WF_LAUNCH(D_, M_) \
+  return launch_early(wfk::wf_fp8_block_append_kernel<D_, M_>, blocks, th, 0, s, p)
   if (pool->head_dim == 128) {
     if (mode == wfk::kRopeNone) WF_LAUNCH(128, wfk::kRopeNone);
-    else if (mode == wfk::kRopeInterleaved) WF_LAUNCH(128, wfk::kRopeInterleaved);
-    else if (mode == wfk::kRopeSplit) WF_LAUNCH(128, wfk::kRopeSplit);
-    else WF_LAUNCH(128, wfk::kRopeSplitPartial);
+    if (mode == wfk::kRopeInterleaved) WF_LAUNCH(128, wfk::kRopeInterleaved);
+    if (mode == wfk::kRopeSplit) WF_LAUNCH(128, wfk::kRopeSplit);
+    WF_LAUNCH(128, wfk::kRopeSplitPartial);
   } else {
     if (mode == wfk::kRopeNone) WF_LAUNCH(64, wfk::kRopeNone);
-    else if (mode == wfk::kRopeInterleaved) WF_LAUNCH(64, wfk::kRopeInterleaved);
-    else if (mode == wfk::kRopeSplit) WF_LAUNCH(64, wfk::kRopeSplit);
-    else WF_LAUNCH(64, wfk::kRopeSplitPartial);
+    if (mode == wfk::kRopeInterleaved) WF_LAUNCH(64, wfk::kRopeInterleaved);
+    if (mode == wfk::kRopeSplit) WF_LAUNCH(64, wfk::kRopeSplit);
+    WF_LAUNCH(64, wfk::kRopeSplitPartial);
   }
 #undef WF_LAUNCH
-  return cudaGetLastError() == cudaSuccess ? WF_OK : WF_ERR_CUDA;
 }
 
 }  // extern "C"
@@ -1839,27 +1861,8 @@ size_t fp8_workspace_bytes(const SegmentList& sl, const Fp8Plan& plan, int Hq, i
 template <int D, int NT>
 int launch_few(const wfk::AttnFewParams& p, cudaStream_t s) {
   const unsigned grid = static_cast<unsigned>(p.tiles) * p.Hk * p.splits;
-  wfk::wf_attn_fp8_few_kernel<D, NT><<<grid, wfk::kFewThreads, wfk::FewSmem<D, NT>::ALLOC, s>>>(p);
-  return cudaGetLastError() == cudaSuccess ? WF_OK : WF_ERR_CUDA;
-}
-
-// A launch whose blocks may take their places while the kernel before it still runs.
-template <typename... Args, typename... Given>
-int launch_early(void (*kernel)(Args...), dim3 grid, int threads, cudaStream_t s, Given... given) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(static_cast<unsigned>(threads));
-  cfg.stream = s;
-  cudaLaunchAttribute attr = {};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kernel, static_cast<Args>(given)...) != cudaSuccess) {
-    cudaGetLastError();
-    return WF_ERR_CUDA;
-  }
-  return WF_OK;
+  return launch_early(wfk::wf_attn_fp8_few_kernel<D, NT>, dim3(grid), wfk::kFewThreads,
+                      wfk::FewSmem<D, NT>::ALLOC, s, p);
 }
 
 // The join of the few-row kernel's parts.
@@ -1867,7 +1870,7 @@ template <int D>
 int launch_join(const wfk::AttnFewParams& p, cudaStream_t s) {
   static_assert(kMaxFp8Splits <= wfk::kMaxJoin, "parts");
   return launch_early(wfk::wf_join_kernel<D>, dim3(static_cast<unsigned>(p.T_q) * p.Hq),
-                      wfk::kJoinThreads, s, p.part_o, p.part_lse, p.splits, p.T_q, p.Hq, p.out,
+                      wfk::kJoinThreads, 0, s, p.part_o, p.part_lse, p.splits, p.T_q, p.Hq, p.out,
                       p.lse);
 }
 
@@ -1919,10 +1922,9 @@ int launch_fp8_blocks(const wfk::AttnFewParams& a, const Fp8Plan& plan, cudaStre
   std::memcpy(p.share_tile, plan.share_tile, sizeof(int) * plan.ctas);
   std::memcpy(p.share_tiles, plan.share_tiles, sizeof(int) * plan.ctas);
   std::memcpy(p.share_slot, plan.share_slot, sizeof(int) * plan.ctas);
-  wfk::wf_attn_fp8_kernel<D>
-      <<<static_cast<unsigned>(plan.ctas), wfk::kFp8AttnThreads, wfk::AttnFp8Smem<D>::ALLOC, s>>>(p);
-  if (cudaGetLastError() != cudaSuccess) return WF_ERR_CUDA;
-  if (plan.n_cut == 0) return WF_OK;
+  const int rc = launch_early(wfk::wf_attn_fp8_kernel<D>, dim3(static_cast<unsigned>(plan.ctas)),
+                              wfk::kFp8AttnThreads, wfk::AttnFp8Smem<D>::ALLOC, s, p);
+  if (rc || plan.n_cut == 0) return rc;
   wfk::Fp8JoinParams j;
   j.units = plan.units;
   j.part_o = a.part_o;
@@ -1937,7 +1939,7 @@ int launch_fp8_blocks(const wfk::AttnFewParams& a, const Fp8Plan& plan, cudaStre
   return launch_early(wfk::wf_piece_join_kernel<D>,
                       dim3(static_cast<unsigned>(plan.n_cut),
                            wfk::kUnitTileRows / wfk::kPieceJoinRows),
-                      wfk::kPieceJoinRows * D / 4, s, j);
+                      wfk::kPieceJoinRows * D / 4, 0, s, j);
 }
 
 }  // namespace

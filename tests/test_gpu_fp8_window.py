@@ -148,3 +148,54 @@ def test_layers_share_a_pool_and_calls_may_share_a_stream():
         assert torch.equal(gout, alone[0])
     assert check_status() == WF_OK
 
+
+
+def test_a_decode_step_in_a_graph_between_other_work():
+    """Memory copies, fills, other kernels and another stream's work before, between and after the calls of
+    a captured step: every call sees what was written before it, replay after replay."""
+    Hq, H, D, ps, N = 8, 2, 128, 16, 200
+    pages = -(-N // ps)
+    rule = NormRope(rotation_table(N, (64,)))
+    pool = PagedPoolFp8Block(pages, ps, H, D)
+    pt = torch.randperm(pages).int().view(1, -1).cuda()
+    proj = torch.zeros(1, Hq + 2 * H, D, dtype=torch.bfloat16, device="cuda")
+    host = torch.zeros(proj.shape, dtype=torch.bfloat16).pin_memory()
+    q = torch.zeros(1, Hq, D, dtype=torch.bfloat16, device="cuda")
+    out, copy = torch.zeros_like(q), torch.zeros_like(q)
+    before = Fp8BlockLayer(pool, pt, 0, [0, N - 1], [0], 0)
+    before.append(0, 1, bf16_rows(N - 1, H, D, 1).cuda(), bf16_rows(N - 1, H, D, 2).cuda())
+    lay = Fp8BlockLayer(pool, pt, 0, [0, N - 1, N], [0, 0], 1)
+    pos = torch.full((1, 1), N - 1, dtype=torch.int32, device="cuda")
+    ws = torch.empty(max(lay.workspace_size(Hq), 16), dtype=torch.uint8, device="cuda")
+
+    def step():
+        proj.copy_(host, non_blocking=True)                       # a copy, then our kernel
+        qk_norm_rope(proj[:, :Hq], q, None, None, rule, pos)
+        out.zero_()                                               # a fill, then our kernels
+        lay.append(1, 2, proj[:, Hq:Hq + H], proj[:, Hq + H:], rule, pos)
+        lay.forward(q, out, workspace=ws)
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            copy.copy_(out)                                       # another stream reads the result
+            qk_norm_rope(copy, copy, None, None, rule, pos)
+        torch.cuda.current_stream().wait_stream(side)
+        copy.mul_(2)
+    side = torch.cuda.Stream()
+    step()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for i in range(6):
+        host.copy_(bf16_rows(1, Hq + 2 * H, D, 10 + i))
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        got = (q.clone(), out.clone(), copy.clone())
+        step()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, (q, out, copy)))
+        vals = [oc.decode_rows(c.cpu().numpy(), s.cpu().numpy(), pt[0].cpu().numpy(), N)
+                for c, s in ((pool.k_codes, pool.k_scale), (pool.v_codes, pool.v_scale))]
+        want, _ = oc.attention(q.double().cpu().numpy(), *vals, [1], [N], D ** -0.5)
+        assert np.abs(out.double().cpu().numpy() - want).max() <= 2.0 ** -7
+    assert check_status() == WF_OK
