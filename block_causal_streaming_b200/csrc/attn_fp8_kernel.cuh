@@ -108,7 +108,7 @@ struct AttnFp8Params {
   int T_q, Hq, Hk, page_size, num_pages, total_rows, box_rows;
   float sl2;                         // scale * log2(e)
   Fp8Units units;
-  int n_units, n_whole;              // units that see keys; the first n_whole go out whole
+  int n_whole;                       // the first n_whole units that see keys go out whole
   int n_blank;                       // units that see none
   // share of CTA i in the tiles of units n_whole ..: from tile share_tile[i] of unit share_unit[i],
   // share_tiles[i] of them; its parts of units go to the slots from share_slot[i] on

@@ -147,8 +147,7 @@ __global__ void __launch_bounds__(kNormRopeThreads, kFp8AppendCtas)
     for (int i = threadIdx.x; i < kFp8BlockTokens * per_row; i += kNormRopeThreads) {
       const int r = i / per_row, j = i - r * per_row;
       float4 cs = make_float4(1.f, 1.f, 0.f, 0.f);
-      if (2 * j < p.rule.pairs)
-      if (r >= n0 && r < n1) {
+      if (2 * j < p.rule.pairs && r >= n0 && r < n1) {
         int pos[3];
         if (load_positions(p.rule, tok0 + r - p.token0, pos)) cs = load_pairs(p.rule, pos, 2 * j);
         else bad = true;

@@ -1915,7 +1915,6 @@ int launch_fp8_blocks(const wfk::AttnFewParams& a, const Fp8Plan& plan, cudaStre
   p.num_pages = a.num_pages;
   p.sl2 = a.sl2;
   p.units = plan.units;
-  p.n_units = plan.n_units;
   p.n_whole = plan.n_whole;
   p.n_blank = plan.n_blank;
   std::memcpy(p.share_unit, plan.share_unit, sizeof(int) * plan.ctas);

@@ -218,6 +218,27 @@ class WavefrontLayer:
                                 self.desc, scale, out, splits, ws, lse, stream)
 
 
+def _scratch(kept: dict, need: int, device, stream) -> torch.Tensor:
+    """Workspace of ``need`` bytes for a call on ``stream`` (None: the current one).
+
+    ``kept`` holds one for each stream, whose calls follow one another; it grows, and a smaller one
+    is given back to the allocator of its own stream.  A call that is being captured gets one of its
+    own from the graph's memory, so that graphs share none with one another or with other calls.
+    """
+    if stream is not None:
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(getattr(stream, "cuda_stream", stream), device)
+        with torch.cuda.stream(stream):
+            return _scratch(kept, need, device, None)
+    if torch.cuda.is_current_stream_capturing():
+        return torch.empty(need, dtype=torch.uint8, device=device)
+    key = torch.cuda.current_stream(device).cuda_stream, device
+    ws = kept.get(key)
+    if ws is None or ws.numel() < need:
+        ws = kept[key] = torch.empty(need, dtype=torch.uint8, device=device)
+    return ws
+
+
 class Fp8BlockLayer:
     """One layer of a wavefront over an FP8 cache that attention reads in place.
 
@@ -236,7 +257,7 @@ class Fp8BlockLayer:
         first = off[num_ctx_chunks]
         self.segments = _abi.Segments([e - first for e in off[num_ctx_chunks + 1:]],
                                       off[num_ctx_chunks + 1:], off[-1], page_tables.shape[1])
-        self._workspace: Optional[torch.Tensor] = None
+        self._workspaces: dict = {}
 
     def append(self, chunk_begin: int, chunk_end: int, k: torch.Tensor, v: torch.Tensor, rule=None,
                positions=None, k_weight=None, stream=None) -> None:
@@ -253,17 +274,14 @@ class Fp8BlockLayer:
                 lse: Optional[torch.Tensor] = None, splits: int = 0,
                 workspace: Optional[torch.Tensor] = None, segments=None, stream=None) -> None:
         """Attention of ``q`` over this layer's cache: the wavefront's query chunks, each up to its
-        own end, or the rows of ``segments``.  Without ``workspace`` the layer allocates one and
-        reuses it; calls and captured graphs that may run at the same time need one each."""
+        own end, or the rows of ``segments``.  Without ``workspace`` the layer keeps one for each
+        stream, and a captured call has its own."""
         if scale is None:
             scale = 1.0 / math.sqrt(self.pool.head_dim)
         seg = segments or self.segments
         if workspace is None:
             need = self.workspace_size(q.shape[1], seg, splits)
             if need > 0:
-                if self._workspace is None or self._workspace.numel() < need or \
-                        self._workspace.device != q.device:
-                    self._workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-                workspace = self._workspace
+                workspace = _scratch(self._workspaces, need, q.device, stream)
         _abi.attn_forward_fp8_block(q, *self.pool.tensors, self.page_tables[self.layer], seg, scale,
                                     out, lse, splits, workspace, stream)

@@ -200,7 +200,7 @@ class RollingCache:
         else:
             self.pool = PagedPool(window.pages * self.num_layers, window.page_size, heads,
                                   head_dim, device, fill=fill)
-        self._workspace: Optional[torch.Tensor] = None
+        self._workspaces: dict = {}
         if page_tables is None:
             page_tables = torch.arange(window.pages * self.num_layers, dtype=torch.int32)
             page_tables = page_tables.view(self.num_layers, window.pages)
@@ -245,6 +245,7 @@ class RollingCache:
                    positions, k_weight) -> None:
         """A round with an FP8 cache or with keys that are normed and rotated on the way in."""
         from . import _abi
+        from .layer import _scratch
         L = self.window.chunk_len
 
         def append(slot, i):
@@ -265,9 +266,8 @@ class RollingCache:
                                 self.page_tables.shape[1])
         if self.fp8_block:
             need = lay.workspace_size(q.shape[1], seg)
-            if need and (self._workspace is None or self._workspace.numel() < need):
-                self._workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-            lay.forward(q, out, scale, lse, 0, self._workspace if need else None, seg, stream)
+            ws = _scratch(self._workspaces, need, q.device, stream) if need else None
+            lay.forward(q, out, scale, lse, 0, ws, seg, stream)
         elif seg is not None:
             if scale is None:
                 scale = 1.0 / math.sqrt(self.pool.head_dim)

@@ -199,3 +199,49 @@ def test_a_decode_step_in_a_graph_between_other_work():
         want, _ = oc.attention(q.double().cpu().numpy(), *vals, [1], [N], D ** -0.5)
         assert np.abs(out.double().cpu().numpy() - want).max() <= 2.0 ** -7
     assert check_status() == WF_OK
+
+
+def test_one_layer_in_two_graphs_and_on_two_streams_without_a_workspace_given():
+    """Calls that leave the workspace to the layer: two captured graphs replayed at the same time, calls
+    on two other streams beside them, and a larger call afterwards, which must not take the graphs'
+    memory."""
+    Hq, H, D, ps, N = 16, 4, 128, 16, 4096
+    pages = N // ps
+    pool = PagedPoolFp8Block(pages, ps, H, D)
+    pt = torch.randperm(pages).int().view(1, -1).cuda()
+    lay = Fp8BlockLayer(pool, pt, 0, [0, N - 4, N], [0, 0], 1)
+    lay.append(0, 2, bf16_rows(N, H, D, 1).cuda(), bf16_rows(N, H, D, 2).cuda())
+    q = [bf16_rows(4, Hq, D, 3 + i).cuda() for i in range(4)]
+    assert lay.workspace_size(Hq) > 0                             # keys are cut
+    want = []
+    for x in q:
+        want.append(torch.empty_like(x))
+        lay.forward(x, want[-1], workspace=torch.empty(lay.workspace_size(Hq), dtype=torch.uint8,
+                                                       device="cuda"))
+    out = [torch.empty_like(x) for x in q]
+    graphs = []
+    for i in range(2):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[i]):
+            lay.forward(q[i], out[i])
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    big = bf16_rows(300, Hq, D, 9).cuda()
+    big_out = torch.empty_like(big)
+    from block_causal_streaming_b200 import Segments
+    seg = Segments([300], [N], N, pages)
+    for rnd in range(6):
+        for o in out:
+            o.zero_()
+        torch.cuda.synchronize()
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                graphs[i].replay()
+        with torch.cuda.stream(streams[2]):
+            lay.forward(q[2], out[2])
+        lay.forward(q[3], out[3], stream=streams[3])
+        if rnd == 2:                                              # a larger workspace from now on
+            lay.forward(big, big_out, segments=seg)
+            torch.empty(1 << 24, dtype=torch.uint8, device="cuda").fill_(255)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
+    assert check_status() == WF_OK
