@@ -18,10 +18,16 @@
 //
 // Two warps per (block, head, tensor), 8 rows each: the rows sit in registers as fp32 (D/16 lanes per
 // row, as in the bf16 pass), so the block is read once; the scale is two warp reductions and a
-// barrier of the pair away.  A CTA takes one block's heads; the 16 tokens' cos and sin wait in shared
-// memory for all of them, and each head's values are asked for while the one before is worked on.
-// (One warp for all 16 rows holds 64 values a lane: 16 warps an SM, and 65 us against 43 on 23 400
-// tokens of 12 heads of 128.)
+// barrier away.  A CTA takes one block's heads; the 16 tokens' cos and sin wait in shared memory for
+// all of them, and each head's values are asked for while the one before is worked on.  Heads of K and
+// of V alternate, and at any time half the warp pairs work on K, so that arithmetic (K) and plain
+// copying (V) share the SM.
+//
+// On 23 400 tokens of 12 heads of 128, 3 axes: 50.6 us, 216 MB, 4.3 TB/s; 51.4 with all K before all V,
+// 65 with one warp for all 16 rows (64 values a lane).  Bound by how loads and arithmetic overlap: the
+// issue slots are half full and HBM is at 0.65 of a copy.  Neither more warps (3 CTAs an SM: 53.1) nor
+// more heads asked for ahead (2 through shared memory 53.1, 3 54.9, 5 62.9) nor 4 warps to a block
+// (55.7) did better.
 #pragma once
 
 #include <cuda_fp8.h>
@@ -43,7 +49,7 @@ struct Fp8BlockAppendParams {
   int weight_per_head;
   int token0, tokens, live;   // appended: [token0, token0 + tokens); live: [0, live)
   int H, page_size, num_pages;
-  int items;                  // (head, tensor) rows per CTA
+  int items;                  // (head, tensor) rows per CTA: 2 H or a multiple of 4
   const int* pt_row;
   int* status;
 };
@@ -86,7 +92,7 @@ __device__ __forceinline__ float exp2_int(int e) {     // 2^e, e in [-126, 127]
   return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
 
-// grid: (blocks of 16 tokens, runs of p.items (head, tensor) rows; K rows first).
+// grid: (blocks of 16 tokens, runs of p.items (head, tensor) rows).
 template <int D, int kMode>
 __global__ void __launch_bounds__(kNormRopeThreads, kFp8AppendCtas)
     wf_fp8_block_append_kernel(const __grid_constant__ Fp8BlockAppendParams p) {
@@ -117,8 +123,10 @@ __global__ void __launch_bounds__(kNormRopeThreads, kFp8AppendCtas)
 
   uint4 lo[STEPS], hi[STEPS];
   const bool whole = n1 - n0 == kFp8BlockTokens;
+  // The CTA's rows alternate between K and V, for every second round of the pairs the other way round.
+  const auto which_of = [&](int hh) { return (hh ^ (hh >> 2)) & 1; };
   const auto load = [&](int hh) {
-    const int which = hh >= p.H ? 1 : 0, h = hh - which * p.H;
+    const int which = which_of(hh), h = hh >> 1;
     const RowSet& s = p.set[which];
     const __nv_bfloat16* src =
         s.src + static_cast<int64_t>(tok0 + r0 - p.token0) * s.stride + (h * D + 8 * sub);
@@ -166,7 +174,7 @@ __global__ void __launch_bounds__(kNormRopeThreads, kFp8AppendCtas)
   int turn = 0;
 #pragma unroll 1
   for (int hh = hh0 + pair; hh < hh1; hh += kFp8AppendPairs, turn ^= 1) {
-    const int which = hh >= p.H ? 1 : 0, h = hh - which * p.H;
+    const int which = which_of(hh), h = hh >> 1;
     uint8_t* const codes = p.codes[which] + code0 + h * D;
     uint8_t* const scale = p.scale[which] + scale0 + h;
     Row x[STEPS];
