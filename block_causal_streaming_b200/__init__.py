@@ -17,7 +17,12 @@ The product is the C-ABI library ``libwf_b200.so`` (declared in ``include/wf.h``
 * ``wf_qk_quantize_i8`` / ``wf_attn_forward_i8`` -- the INT8 tier: smoothed int8 K and int8 Q
   with per-128-row scales, QK^T as an integer product on the tensor core;
   ``wf_qk_quantize_e4m3`` / ``wf_attn_forward_e4m3`` the FP8 tier: e4m3 Q and K with
-  per-128-row scales, QK^T on the tensor core's 8-bit floating format.
+  per-128-row scales, QK^T on the tensor core's 8-bit floating format;
+* ``wf_qk_norm_rope`` / ``wf_kv_append_rope`` -- norms of q and k for each head with the position
+  rotation, and the same for keys on their way into the pages;
+  ``wf_kv_append_fp8_block`` / ``wf_attn_forward_fp8_block`` an FP8 cache (e4m3, one power-of-two
+  scale per 16 tokens and head) and attention that reads it in place, one query token to whole
+  wavefronts.
 
 This package is its thin Python binding (ctypes, argument marshalling only), a small helper that
 owns the paged pools of one layer (:mod:`.layer`), the round-by-round planner of a streaming

@@ -7,8 +7,8 @@
 //   - QK^T runs on the codes as they are (kind::f8f6f4).  A bf16 query value has 8 significant bits
 //     and e4m3 has 4, so each row is split once into two e4m3 rows, hi + lo, under a power of two
 //     for the row; S = hi K^T + lo K^T is the exact product for values down to 2^-10 of the row's
-//     largest (and within 2^-18 of that largest below), at the time of one bf16 product.  Four
-//     threads' worth of conversion per key and tile would be the other way (K to bf16).
+//     largest (and within 2^-18 of that largest below), at the time of one bf16 product.  The other
+//     way, K to bf16 in shared memory, would double the converters' work and take 16 KB a tile more.
 //   - The key scale of each 16 keys multiplies its 16 columns of S, inside the multiply-add that
 //     subtracts the maximum; the maximum is taken over the 8 blocks' scaled maxima.
 //   - Values go to f16 (exact) in shared memory, by four converter warps: 16 codes a step, times
@@ -33,6 +33,15 @@
 // launch.  So the SMs end together whatever the number of units (228 units of equal length on 148
 // SMs: 1.54 units each, where whole units take 2 turns and uniform parts 4 to 5 percent of joining
 // and 10 of idle SMs), and loads run ahead from one piece into the next.
+//
+// Bound by the exponentials (MUFU) and the tensor pipe together, both three quarters busy, in a chain
+// that passes one S buffer between two Q tiles, and in long runs by the power limit.  12 heads of 128:
+// the 5-chunk wavefront (23 400 rows, up to 32 760 keys, 3.36 TFLOP) 2.79 ms on a cool GPU, 3.07 in a
+// loop at about 1.64 GHz (0.73 and 0.66 of a cuBLAS bf16 product; the bf16 kernel takes 2.99 in the same
+// loop); one chunk of 4680 rows against 37 440 keys 854 us cool, 0.99 ms in a loop.
+// Steps on the way (the wavefront unless said otherwise): row sums with packed adds 3.50 -> 3.11 ms;
+// pieces instead of uniform parts, one chunk 1000 -> 854 us; loops that fit the instruction cache
+// (compact waits, one piece loop for the eight warps that are not softmax) were worth a factor 1.7.
 //
 // Warp roles (512 threads): 0-3, 4-7 softmax of Q tile 0, 1 (thread = row; they also split Q);
 // 8 TMA of K, key scales; 9 issues QK^T; 10 issues P.V; 11 TMA of V codes; 12-15 convert V.  Rings

@@ -1714,7 +1714,8 @@ constexpr int kFewRows = 32;
 // us; 512 rows 128 / 114 / 113 / 117; 4680 rows 863 / 857 / 854 / 866.
 constexpr int kPieceCost = 8;
 
-// Units a CTA from which on none is cut: whole ones are then even enough.
+// Units a CTA from which on none is cut: whole ones then end within 1/48 of one another, less than what
+// parts and their join cost, and the plan's time and memory stay bounded.
 constexpr int kWholeUnits = 48;
 
 // Spreads the key tiles of the row blocks over `ctas` CTAs (see the kernel): `n_whole` units go out

@@ -32,9 +32,10 @@
  *     errors are detected on the host before anything is launched.  Errors found by a kernel
  *     (a page index outside the pool, a bounded wait that ran out) are recorded in a per-device
  *     status word read by wf_check_status.
- *   - Attention computes in bf16 with fp32 accumulation; FP8 appears only in the K/V transport
- *     calls (wf_kv_append_fp8, wf_kv_dequant and their chunk-range forms).  Batch 1, one layer
- *     per call.
+ *   - Attention computes in bf16 with fp32 accumulation.  8-bit formats appear in the K/V
+ *     transport calls (wf_kv_append_fp8, wf_kv_dequant and what follows them), in the INT8 and FP8
+ *     attention tiers (Q and K) and in the FP8 cache (K and V, wf_kv_append_fp8_block and
+ *     wf_attn_forward_fp8_block).  Batch 1, one layer per call.
  */
 #ifndef WF_H_
 #define WF_H_
@@ -577,8 +578,9 @@ int wf_kv_append_fp8_block(const wf_kv_pool_fp8_block_t* pool, int layer, int ch
  *   segments        as in wf_attn_forward_segments, except that a limit may also be 0 (the rows see
  *                   no key: out 0, lse -inf) and limits may come in any order.
  *   out             device bf16, laid out as q: softmax(scale q K^T) V over the rows' keys, on the
- *                   values the cache stands for.  fp32 statistics and accumulation; weights are
- *                   rounded to 11 bits or more before P.V.
+ *                   values the cache stands for.  Statistics, sums and accumulation are fp32; the
+ *                   weights go into P.V with 11 bits down to 2^-27 of the row's largest and in steps
+ *                   of 2^-37 of it below.
  *   lse_or_null     device fp32 [num_q_heads][rows] (optional).
  *   splits          1: no row's keys are cut (no workspace).  0: the library cuts them so that the
  *                   SMs are filled, and joins the parts in a second launch.  S > 1: with up to 32
