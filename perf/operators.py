@@ -247,7 +247,9 @@ def prepare(case, seed):
         s["rows_end"], s["kv_end"] = _limits(case)
         if own:
             from block_causal_streaming_b200 import Segments, attn_fp8_block_workspace_size
-            s["seg"] = Segments(s["rows_end"], s["kv_end"], case["keys"], s["pages"])
+            # a segment that ends before one in front of it takes that one's rows over
+            ends = [min(s["rows_end"][i:]) for i in range(len(s["rows_end"]))]
+            s["seg"] = Segments(ends, s["kv_end"], case["keys"], s["pages"])
             need = attn_fp8_block_workspace_size(s["seg"], hq, hk, d)
             s["workspace"] = torch.empty(need, dtype=torch.uint8, device="cuda") if need else None
     return s
