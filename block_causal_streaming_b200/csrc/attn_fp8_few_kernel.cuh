@@ -175,7 +175,8 @@ struct FewSmem {
   static constexpr uint32_t L_OFF = M_OFF + kFewWarps * NT * 32u;
   static constexpr uint32_t BAR_OFF = L_OFF + kFewWarps * NT * 32u;  // [warps][NS]
   static constexpr uint32_t MISC_OFF = BAR_OFF + 8u * kFewWarps * NS;
-  static constexpr uint32_t BYTES = MISC_OFF + 16u;
+  static constexpr uint32_t E_OFF = MISC_OFF + 16u;          // exponents of the warps' outputs
+  static constexpr uint32_t BYTES = E_OFF + kFewWarps * 4u;
   static constexpr uint32_t ALLOC = BYTES + 1024;            // slack for 1024-byte alignment
   static_assert(kFewWarps * NT * 8u * OPITCH * 4u <= RING, "outputs fit the ring");
   static_assert(ALLOC <= (CTAS == 2 ? 113u : 227u) * 1024u, "shared memory per CTA");
@@ -456,7 +457,8 @@ __global__ void __launch_bounds__(kFewThreads, FewSmem<D, NT>::CTAS)
   float* const sm_m = reinterpret_cast<float*>(few_smem + L::M_OFF);
   float* const sm_l = reinterpret_cast<float*>(few_smem + L::L_OFF);
   float* const sm_o = reinterpret_cast<float*>(few_smem + L::O_OFF);
-  const float unscale = pow2f(E);                 // sums and outputs share the factor 2^13
+  int* const sm_e = reinterpret_cast<int*>(few_smem + L::E_OFF);
+  if (lane == 0) sm_e[warp] = E;
 #pragma unroll
   for (int a = 0; a < NT; ++a)
 #pragma unroll
@@ -474,12 +476,17 @@ __global__ void __launch_bounds__(kFewThreads, FewSmem<D, NT>::CTAS)
 #pragma unroll
       for (int j = 0; j < D / 16; j += 2)
         *reinterpret_cast<float4*>(dst + 2 * j) =
-            make_float4(o[a][j][r] * unscale, o[a][j][2 + r] * unscale,
-                        o[a][j + 1][r] * unscale, o[a][j + 1][2 + r] * unscale);
+            make_float4(o[a][j][r], o[a][j][2 + r], o[a][j + 1][r], o[a][j + 1][2 + r]);
     }
   __syncthreads();
   constexpr int PER = D / 32;
   if (!ok) return;                                // a wait ran out: recorded, nothing is written
+  // outputs stand for o 2^E; sums and outputs share the factor 2^13.  2^E is multiplied in after the
+  // division, so that values near the largest that fp32 holds do not overflow in the sum.
+  int e_max = sm_e[0];
+#pragma unroll
+  for (int w = 1; w < kFewWarps; ++w) e_max = max(e_max, sm_e[w]);
+  const float size = pow2f(e_max);
   for (int m = warp; m < R && m0 + m < m_total; m += kFewWarps) {
     float top = -INFINITY;
 #pragma unroll
@@ -492,9 +499,10 @@ __global__ void __launch_bounds__(kFewThreads, FewSmem<D, NT>::CTAS)
     for (int w = 0; w < kFewWarps; ++w) {
       const float wt = ex2_approx(sm_m[w * R + m] - ref);
       l += wt * sm_l[w * R + m];
+      const float wo = wt * pow2f(sm_e[w] - e_max);
 #pragma unroll
       for (int c = 0; c < PER; ++c)
-        acc[c] = fmaf(wt, sm_o[(w * R + m) * L::OPITCH + lane * PER + c], acc[c]);
+        acc[c] = fmaf(wo, sm_o[(w * R + m) * L::OPITCH + lane * PER + c], acc[c]);
     }
     // a row that sees no key (of this part): 0, log-sum-exp -inf; a NaN sum stays NaN
     const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -504,14 +512,14 @@ __global__ void __launch_bounds__(kFewThreads, FewSmem<D, NT>::CTAS)
     if (p.splits > 1) {
       float* dst = p.part_o + (static_cast<int64_t>(split) * p.T_q * p.Hq + orow) * D + lane * PER;
 #pragma unroll
-      for (int c = 0; c < PER; ++c) dst[c] = acc[c] * inv;
+      for (int c = 0; c < PER; ++c) dst[c] = acc[c] * inv * size;
       if (lane == 0)
         p.part_lse[(static_cast<int64_t>(split) * p.Hq + h) * p.T_q + row] = lse;
     } else {
       uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + orow * D + lane * PER);
 #pragma unroll
       for (int c = 0; c < PER / 2; ++c)
-        dst[c] = pack_bf16x2(acc[2 * c] * inv, acc[2 * c + 1] * inv);
+        dst[c] = pack_bf16x2(acc[2 * c] * inv * size, acc[2 * c + 1] * inv * size);
       if (lane == 0 && p.lse != nullptr) p.lse[static_cast<int64_t>(h) * p.T_q + row] = lse;
     }
   }
@@ -523,6 +531,9 @@ __global__ void __launch_bounds__(kFewThreads, FewSmem<D, NT>::CTAS)
 // parts one after the other: 18 us for 32 rows of 37 parts, against 3 here.)
 constexpr int kJoinThreads = 256;
 constexpr int kMaxJoin = 256;                       // parts
+// Parts are summed with weights made smaller by this power of two, so that the sum of the most parts
+// stays in range whatever the values.
+constexpr float kJoinDown = 1.f / kMaxJoin, kJoinUp = kMaxJoin;
 
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads)
@@ -545,7 +556,7 @@ __global__ void __launch_bounds__(kJoinThreads)
   for (int i = 0; i < kJoinThreads / 32; ++i) top = fmaxf(top, red[i]);
   const float ref = top == -INFINITY ? 0.f : top;
   const float w = expf(ls - ref);
-  if (tid < splits) wt[tid] = w;
+  if (tid < splits) wt[tid] = w * kJoinDown;
   float sum = w;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -580,7 +591,7 @@ __global__ void __launch_bounds__(kJoinThreads)
 #pragma unroll
     for (int i = 0; i < kJoinThreads / 32; ++i) v += acc_s[i][tid];
     out[(static_cast<int64_t>(row) * Hq + h) * D + tid] =
-        __float2bfloat16_rn(total == 0.f ? 0.f : v / total);
+        __float2bfloat16_rn(total == 0.f ? 0.f : v / total * kJoinUp);
   }
   if (tid == 0 && lse != nullptr)
     lse[static_cast<int64_t>(h) * T_q + row] = total == 0.f ? -INFINITY : ref + logf(total);

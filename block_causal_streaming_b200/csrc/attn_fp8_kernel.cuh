@@ -791,14 +791,16 @@ __global__ void __launch_bounds__(kPieceJoinRows * D / 4)
     for (int i = 0; i < 8; ++i) {
       if (s0 + i >= parts) break;
       const float w = expf(wt[s0 + i][tr] - ref);
+      const float d = w * kJoinDown;
       total += w;
-      acc.x = fmaf(w, x[i].x, acc.x);
-      acc.y = fmaf(w, x[i].y, acc.y);
-      acc.z = fmaf(w, x[i].z, acc.z);
-      acc.w = fmaf(w, x[i].w, acc.w);
+      acc.x = fmaf(d, x[i].x, acc.x);
+      acc.y = fmaf(d, x[i].y, acc.y);
+      acc.z = fmaf(d, x[i].z, acc.z);
+      acc.w = fmaf(d, x[i].w, acc.w);
     }
   }
-  const float inv = total == 0.f ? 0.f : 1.f / total;
+  static_assert(kFp8MaxCtas <= kMaxJoin, "parts of a unit");
+  const float inv = total == 0.f ? 0.f : kJoinUp / total;
   const int64_t row = p.units.seg_row0[at.seg] + m / p.units.group;
   const int h = at.head * p.units.group + m % p.units.group;
   *reinterpret_cast<uint2*>(p.out + (row * p.Hq + h) * D + 4 * c) =

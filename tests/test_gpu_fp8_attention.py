@@ -128,6 +128,26 @@ def test_large_logits_and_uneven_blocks(rows):
     check(out, lse, q, vals, [rows], [N], 0.2)
 
 
+@pytest.mark.parametrize("splits", [0, 1])
+@pytest.mark.parametrize("rows", [1, 20, 150])
+@pytest.mark.parametrize("byte", [246, 27, 0], ids=["largest", "smallest", "mixed"])
+def test_values_at_the_ends_of_the_scales_range(rows, byte, splits):
+    """Values up to 448 2^119, just inside fp32, and down to 2^-109: sums over many keys stay in range."""
+    N, H, D, ps = 3000, 2, 128, 16
+    cache, pt, vals = make_cache(N, H, D, ps, 60)
+    live = cache[3] != 255
+    b = torch.full_like(cache[3], byte)
+    if byte == 0:                                           # blocks of both ends side by side
+        b[:, :, 0], b[:, :, 1] = 246, 27
+        b[::2] = 127
+    cache[3].copy_(torch.where(live, b, cache[3]))
+    vals[1] = oc.decode_rows(cache[1].cpu().numpy(), cache[3].cpu().numpy(), pt.cpu().numpy(), N)
+    q = bf16_rows(rows, 2 * H, D, 61).cuda()
+    out, lse = run(q, cache, pt, Segments([rows], [N], N, pt.numel()), D ** -0.5, splits)
+    assert check_status() == WF_OK
+    check(out, lse, q, vals, [rows], [N], D ** -0.5)
+
+
 @pytest.mark.parametrize("rows", [4, 140])
 def test_what_rows_do_not_see_cannot_reach_them(rows):
     """A NaN value and a NaN key in tokens past a segment's limit leave its rows as they were; rows
