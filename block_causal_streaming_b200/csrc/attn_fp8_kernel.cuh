@@ -644,16 +644,17 @@ __global__ void __launch_bounds__(kFp8AttnThreads, 1)
           if (!ok) break;
           const uint32_t src = base + L::C_OFF + cs * L::CTILE;
           const uint32_t dst = base + L::V_OFF + vs * L::VTILE;
-          const bool seen = (pc.kb + j) * BN + key < pc.n_max;   // else zeros, whatever the bytes
+          // zeros past the limit, whatever the bytes
+          const uint32_t seen = (pc.kb + j) * BN + key < pc.n_max ? 0xFFFFFFFFu : 0u;
 #pragma unroll
           for (int c = 0; c < D / 16; ++c) {
             const uint4 v = ld_shared_v4(src + swz<D>(key, c));
-            const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+            const uint32_t in[4] = {v.x & seen, v.y & seen, v.z & seen, v.w & seen};
             uint32_t o[8];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              o[2 * i] = seen ? mul_f16x2(widen2(in[i]), f) : 0u;
-              o[2 * i + 1] = seen ? mul_f16x2(widen2_high(in[i]), f) : 0u;
+              o[2 * i] = mul_f16x2(widen2(in[i]), f);
+              o[2 * i + 1] = mul_f16x2(widen2_high(in[i]), f);
             }
             // f16 channels 16 c .. 16 c + 15: pieces 2 c and 2 c + 1 of the 128-byte halves
             const uint32_t half = dst + static_cast<uint32_t>(c / 4) * L::VHALF;
