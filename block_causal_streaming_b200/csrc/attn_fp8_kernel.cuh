@@ -36,9 +36,10 @@
 //
 // Bound by the exponentials (MUFU) and the tensor pipe together, both three quarters busy, in a chain
 // that passes one S buffer between two Q tiles, and in long runs by the power limit.  12 heads of 128:
-// the 5-chunk wavefront (23 400 rows, up to 32 760 keys, 3.36 TFLOP) 2.79 ms on a cool GPU, 3.07 in a
-// loop at about 1.64 GHz (0.73 and 0.66 of a cuBLAS bf16 product; the bf16 kernel takes 2.99 in the same
-// loop); one chunk of 4680 rows against 37 440 keys 854 us cool, 0.99 ms in a loop.
+// the 5-chunk wavefront (23 400 rows, up to 32 760 keys, 3.36 TFLOP) 2.70-2.79 ms for a single call,
+// 3.05 in a loop at about 1.64 GHz (0.73 and 0.66 of a cuBLAS bf16 product; the bf16 kernel takes 2.99 in
+// the same loop); one chunk of 4680 rows against 37 440 keys 850-910 us in a few calls, 0.98 ms in a loop.
+// A pair of Q tiles takes 3240 cycles for a key tile, with 54 % of the issue slots busy.
 // Steps on the way (the wavefront unless said otherwise): row sums with packed adds 3.50 -> 3.11 ms;
 // pieces instead of uniform parts, one chunk 1000 -> 854 us; loops that fit the instruction cache
 // (compact waits, one piece loop for the eight warps that are not softmax) were worth a factor 1.7.
