@@ -140,7 +140,7 @@ __device__ __forceinline__ float pow2f(int e) {     // 2^e, e clamped to the nor
 template <typename P>
 __device__ __forceinline__ int fp8_row(const P& p, int tok) {
   const int idx = tok / p.page_size;
-  int pg = __ldg(p.page_table + idx);
+  int pg = p.page_table[idx];
   if (pg < 0 || pg >= p.num_pages) {
     atomicCAS(p.status, 0, 5 /* WF_ERR_PAGE_OOB */);
     pg = 0;
@@ -233,8 +233,8 @@ __global__ void __launch_bounds__(kFewThreads, FewSmem<D, NT>::CTAS)
     if (j0 + lane < nk) {
       my_row = fp8_row(p, (lo + (j0 + lane) * kFewWarps) * 16);
       const int64_t at = static_cast<int64_t>(my_row / 16) * p.Hk + head;
-      my_ks = __ldg(p.k_scale + at);
-      my_vs = __ldg(p.v_scale + at);
+      my_ks = p.k_scale[at];
+      my_vs = p.v_scale[at];
     }
   };
   // bring block j, at pool row `row`, into its slot (which every lane has left)
@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(kFewThreads, FewSmem<D, NT>::CTAS)
           p.q + (static_cast<int64_t>(row) * p.Hq + h) * D + lane * PER);
 #pragma unroll
       for (int i = 0; i < PER / 2; ++i) {
-        const uint32_t w = __ldg(src + i);
+        const uint32_t w = src[i];
         x[2 * i] = __uint_as_float(w << 16);
         x[2 * i + 1] = __uint_as_float(w & 0xFFFF0000u);
       }
@@ -537,8 +537,8 @@ constexpr float kJoinDown = 1.f / kMaxJoin, kJoinUp = kMaxJoin;
 
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads)
-    wf_join_kernel(const float* __restrict__ part_o, const float* __restrict__ part_lse, int splits,
-                   int T_q, int Hq, __nv_bfloat16* __restrict__ out, float* __restrict__ lse) {
+    wf_join_kernel(const float* part_o, const float* part_lse, int splits, int T_q, int Hq,
+                   __nv_bfloat16* out, float* lse) {
   constexpr int PER = D / 32;
   __shared__ float wt[kMaxJoin], red[kJoinThreads / 32], acc_s[kJoinThreads / 32][D];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;

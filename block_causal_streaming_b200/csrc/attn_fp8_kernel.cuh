@@ -348,7 +348,7 @@ __global__ void __launch_bounds__(kFp8AttnThreads, 1)
         uint4 x[D / 8];
         const uint4* src = reinterpret_cast<const uint4*>(p.q + orow * D);
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) x[c] = live ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+        for (int c = 0; c < D / 8; ++c) x[c] = live ? src[c] : make_uint4(0, 0, 0, 0);
         uint32_t mw = 0;                                    // largest |x|, as a bit pattern
 #pragma unroll
         for (int c = 0; c < D / 8; ++c) {
@@ -568,7 +568,7 @@ __global__ void __launch_bounds__(kFp8AttnThreads, 1)
           const int tok = (pc.kb + t) * BN + lane * 16;
           if (!is_k || lane >= 8 || t >= nk || tok >= pc.n_max) return 1.f;
           const int r = fp8_row(p, tok);
-          const uint32_t b = __ldg(p.k_scale + static_cast<int64_t>(r / 16) * p.Hk + pc.head);
+          const uint32_t b = p.k_scale[static_cast<int64_t>(r / 16) * p.Hk + pc.head];
           return __uint_as_float(b << 23);
         };
         int coord = box_row(0, lane);                      // looked up one tile ahead
@@ -602,7 +602,7 @@ __global__ void __launch_bounds__(kFp8AttnThreads, 1)
       } else if (warp >= 12) {
         const int first = pc.kb * BN, last = min((pc.kb + nk) * BN, pc.n_max);
         auto exponent = [&](int tok) -> int {              // value scale of a token's block, biased
-          return __ldg(p.v_scale + static_cast<int64_t>(fp8_row(p, tok) / 16) * p.Hk + pc.head);
+          return p.v_scale[static_cast<int64_t>(fp8_row(p, tok) / 16) * p.Hk + pc.head];
         };
         // exponent of this thread's row of a tile, looked up a tile ahead; -1: nothing to see there
         auto row_exponent = [&](int t) -> int {

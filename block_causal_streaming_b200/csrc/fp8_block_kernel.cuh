@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kNormRopeThreads, kFp8AppendCtas)
     }
   };
   if (hh0 + pair < hh1) load(hh0 + pair);
-  const int pg = __ldg(p.pt_row + tok0 / p.page_size);
+  const int pg = p.pt_row[tok0 / p.page_size];
   if (pg < 0 || pg >= p.num_pages) {
     if (threadIdx.x == 0) atomicCAS(p.status, 0, 5 /* WF_ERR_PAGE_OOB */);
     return;

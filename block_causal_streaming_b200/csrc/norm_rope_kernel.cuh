@@ -75,7 +75,7 @@ __device__ __forceinline__ bool load_positions(const NormRope& r, int64_t t, int
   for (int i = 0; i < 3; ++i) {
     pos[i] = 0;
     if (i < r.num_axes) {
-      pos[i] = __ldg(r.positions + t * r.num_axes + i);
+      pos[i] = r.positions[t * r.num_axes + i];
       ok = ok && pos[i] >= 0 && pos[i] < r.table_rows;
     }
   }
@@ -88,10 +88,10 @@ __device__ __forceinline__ float4 load_pairs(const NormRope& r, const int (&pos)
   const int b = i + 1 >= r.axis2 ? pos[2] : i + 1 >= r.axis1 ? pos[1] : pos[0];
   const float2* at = r.table + static_cast<int64_t>(a) * r.pairs + i;
   if (a == b) {
-    const float4 x = __ldg(reinterpret_cast<const float4*>(at));
+    const float4 x = *reinterpret_cast<const float4*>(at);
     return make_float4(x.x, x.z, x.y, x.w);
   }
-  const float2 x = __ldg(at), y = __ldg(r.table + static_cast<int64_t>(b) * r.pairs + i + 1);
+  const float2 x = *at, y = r.table[static_cast<int64_t>(b) * r.pairs + i + 1];
   return make_float4(x.x, y.x, x.y, y.y);
 }
 
@@ -256,8 +256,8 @@ __device__ __forceinline__ void load_weight(const __nv_bfloat16* weight, int64_t
                                             Row& w) {
   uint4 lo = make_uint4(kOnes, kOnes, kOnes, kOnes), hi = lo;
   if (weight != nullptr) {
-    lo = __ldg(reinterpret_cast<const uint4*>(weight + at + 8 * sub));
-    hi = __ldg(reinterpret_cast<const uint4*>(weight + at + 8 * sub + D / 2));
+    lo = *reinterpret_cast<const uint4*>(weight + at + 8 * sub);
+    hi = *reinterpret_cast<const uint4*>(weight + at + 8 * sub + D / 2);
   }
   unpack_row<kMode>(lo, hi, w);
 }
@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(kNormRopeThreads, kNormRopeCtas)
     int64_t row = t;                              // destination row of the token
     if (kAppend) {
       const int tok = p.token0 + static_cast<int>(t);
-      const int pg = __ldg(p.pt_row + tok / p.page_size);
+      const int pg = p.pt_row[tok / p.page_size];
       if (pg < 0 || pg >= p.num_pages) {
         if (lane == 0) atomicCAS(p.status, 0, 5 /* WF_ERR_PAGE_OOB */);
         continue;

@@ -22,6 +22,8 @@ __device__ __forceinline__ uint64_t globaltimer_ns() {
 
 // Launches that overlap the kernel before them: wait until that kernel has ended and its writes are
 // visible (nothing it writes may be touched before), and let the next such launch take its places.
+// Such a kernel begins while its inputs may still be written, so it reads them all with ordinary loads:
+// the read-only path (__ldg, const __restrict__) is for what nobody writes during the whole kernel.
 __device__ __forceinline__ void wait_for_previous() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
