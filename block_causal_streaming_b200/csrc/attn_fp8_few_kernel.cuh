@@ -283,7 +283,9 @@ __global__ void __launch_bounds__(kFewThreads, FewSmem<D, NT>::CTAS)
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     const int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
     const int up = top > 0.f ? min(14 - e, 126) : 0;
-    const float f = pow2f(up);
+    // An infinite value makes its row NaN: as a logit of -inf for every key it would look like a row
+    // that sees none.
+    const float f = top < INFINITY ? pow2f(up) : __uint_as_float(0x7FFFFFFFu);
     if (lane == 0) qfac[m] = pow2f(-up) * p.sl2;
     // channels c, c + 1 of row m: fragment of step (c / 64) 4 + (c % 16) / 4
 #pragma unroll
