@@ -1420,9 +1420,9 @@ int norm_rope_rule(const wf_norm_rope_t* rule, const int32_t* positions, int D,
   out->num_axes = rule->num_axes;
   out->axis1 = static_cast<int>(rule->num_axes > 1 ? first[1] : pairs);
   out->axis2 = static_cast<int>(rule->num_axes > 2 ? first[2] : pairs);
-  *mode = rule->interleaved ? wfk::kRopeInterleaved
-          : 2 * pairs == D  ? wfk::kRopeSplit
-                            : wfk::kRopeSplitPartial;
+  const bool whole = 2 * pairs == D;
+  *mode = rule->interleaved ? (whole ? wfk::kRopeInterleaved : wfk::kRopeInterleavedPartial)
+                            : (whole ? wfk::kRopeSplit : wfk::kRopeSplitPartial);
   return WF_OK;
 }
 
@@ -1481,11 +1481,13 @@ int launch_norm_rope(wfk::NormRopeParams* p, wfk::RopeMode mode, int D, const De
     if (mode == wfk::kRopeNone) WF_LAUNCH(128, wfk::kRopeNone);
     if (mode == wfk::kRopeInterleaved) WF_LAUNCH(128, wfk::kRopeInterleaved);
     if (mode == wfk::kRopeSplit) WF_LAUNCH(128, wfk::kRopeSplit);
+    if (mode == wfk::kRopeInterleavedPartial) WF_LAUNCH(128, wfk::kRopeInterleavedPartial);
     WF_LAUNCH(128, wfk::kRopeSplitPartial);
   } else {
     if (mode == wfk::kRopeNone) WF_LAUNCH(64, wfk::kRopeNone);
     if (mode == wfk::kRopeInterleaved) WF_LAUNCH(64, wfk::kRopeInterleaved);
     if (mode == wfk::kRopeSplit) WF_LAUNCH(64, wfk::kRopeSplit);
+    if (mode == wfk::kRopeInterleavedPartial) WF_LAUNCH(64, wfk::kRopeInterleavedPartial);
     WF_LAUNCH(64, wfk::kRopeSplitPartial);
   }
 #undef WF_LAUNCH
@@ -1643,11 +1645,13 @@ int wf_kv_append_fp8_block(const wf_kv_pool_fp8_block_t* pool, int layer, int ch
     if (mode == wfk::kRopeNone) WF_LAUNCH(128, wfk::kRopeNone);
     if (mode == wfk::kRopeInterleaved) WF_LAUNCH(128, wfk::kRopeInterleaved);
     if (mode == wfk::kRopeSplit) WF_LAUNCH(128, wfk::kRopeSplit);
+    if (mode == wfk::kRopeInterleavedPartial) WF_LAUNCH(128, wfk::kRopeInterleavedPartial);
     WF_LAUNCH(128, wfk::kRopeSplitPartial);
   } else {
     if (mode == wfk::kRopeNone) WF_LAUNCH(64, wfk::kRopeNone);
     if (mode == wfk::kRopeInterleaved) WF_LAUNCH(64, wfk::kRopeInterleaved);
     if (mode == wfk::kRopeSplit) WF_LAUNCH(64, wfk::kRopeSplit);
+    if (mode == wfk::kRopeInterleavedPartial) WF_LAUNCH(64, wfk::kRopeInterleavedPartial);
     WF_LAUNCH(64, wfk::kRopeSplitPartial);
   }
 #undef WF_LAUNCH
