@@ -1632,8 +1632,14 @@ int wf_kv_append_fp8_block(const wf_kv_pool_fp8_block_t* pool, int layer, int ch
   p.status = d->status;
   const int64_t nb = (p.token0 + int64_t{p.tokens} - 1) / wfk::kFp8BlockTokens -
                      p.token0 / wfk::kFp8BlockTokens + 1;
-  // one CTA for all heads of a block when the blocks fill the GPU, else one for a head a warp pair
-  p.items = nb >= 2 * d->num_sms ? 2 * p.H : wfk::kFp8AppendPairs;
+  // A CTA takes all heads of a block, so that the block's cos and sin are fetched once and a head's values
+  // while the one before is worked on, or a head a warp pair, so that few blocks fill the SMs too.
+  // Measured, all heads / a head a pair, us in a graph: 12 heads of 128, 63 blocks 7.4 / 6.6, 88 blocks
+  // 8.3 / 7.4, 100 blocks 8.9 / 9.9, 150 blocks 10.6 / 13.7, 293 blocks (a chunk of 4680 tokens) 10.1 /
+  // 19.6; 40 heads of 128, 82 blocks 19.8 / 17.9, 100 blocks 20.9 / 22.6; 12 heads of 64, 125 blocks
+  // 5.8 / 5.5, 200 blocks 8.5 / 8.6, 293 blocks 10.1 / 12.2; 40 heads of 64, 150 blocks 19.2 / 15.9.
+  const bool all_heads = nb * pool->head_dim >= static_cast<int64_t>(80) * d->num_sms;
+  p.items = all_heads ? 2 * p.H : wfk::kFp8AppendPairs;
   const int64_t runs = (2 * static_cast<int64_t>(p.H) + p.items - 1) / p.items;
   if (nb > INT32_MAX || runs > 65535) return WF_ERR_SHAPE;
   const dim3 blocks(static_cast<unsigned>(nb), static_cast<unsigned>(runs));
