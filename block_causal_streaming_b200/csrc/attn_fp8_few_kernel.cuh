@@ -454,7 +454,9 @@ __global__ void __launch_bounds__(kFewThreads, FewSmem<D, NT>::CTAS)
       const int jl = issued - 1 - r;
       few_drain(full(jl % NS), (jl / NS) & 1);
     }
-  __syncthreads();                                // the ring is done with
+  // The ring is done with.  One warp's lost wait is the CTA's: it writes nothing (the parts of other
+  // CTAs, and what a join makes of missing ones, are undefined after a timeout).
+  if (!__syncthreads_and(ok)) return;
   // ---- join the warps
   float* const sm_m = reinterpret_cast<float*>(few_smem + L::M_OFF);
   float* const sm_l = reinterpret_cast<float*>(few_smem + L::L_OFF);
@@ -482,7 +484,6 @@ __global__ void __launch_bounds__(kFewThreads, FewSmem<D, NT>::CTAS)
     }
   __syncthreads();
   constexpr int PER = D / 32;
-  if (!ok) return;                                // a wait ran out: recorded, nothing is written
   // outputs stand for o 2^E; sums and outputs share the factor 2^13.  2^E is multiplied in after the
   // division, so that values near the largest that fp32 holds do not overflow in the sum.
   int e_max = sm_e[0];

@@ -58,11 +58,13 @@ enum {
   WF_ERR_CAPACITY = 4,     /* the layer needs more pages than max_pages_per_seq */
   WF_ERR_PAGE_OOB = 5,     /* device: a page-table entry outside [0, num_pages); that page was not
                               written (append) or was read as page 0 (attention) */
-  WF_ERR_TIMEOUT = 6,      /* device: a bounded wait inside a kernel ran out; the kernel stopped */
+  WF_ERR_TIMEOUT = 6,      /* device: a bounded wait inside a kernel ran out; the kernel stopped.  What
+                              that call had to write (outputs, lse, workspace) is undefined: some
+                              rows may be written, others stale */
   WF_ERR_CUDA = 7,         /* a CUDA runtime or driver call failed */
   WF_ERR_NO_DEVICE = 8,    /* no sm_100 device is current */
-  WF_ERR_POSITION = 9      /* device: a position outside the rotation table; that token was not
-                              written */
+  WF_ERR_POSITION = 9      /* device: a position outside the rotation table; that token (FP8 cache:
+                              its block of 16) was not written */
 };
 
 /* Maximum number of chunks (context + active) in one wavefront descriptor. */
