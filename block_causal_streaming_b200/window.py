@@ -183,15 +183,24 @@ class RollingCache:
     attention for all of them in one launch and, once the ring is full, hands the store chunk into
     the slot of the chunk that leaves.  ``fp8_block``: the K/V stay in an FP8 cache with one scale
     for 16 tokens and head (:class:`layer.PagedPoolFp8Block`), which attention reads in place.
+
+    ``append_runs`` (FP8 cache): a run of consecutive slots is one append, not one a chunk.  Where
+    chunks are no multiple of 16 tokens, a block that two new chunks share is then coded once, from
+    both.  Chunk by chunk it is coded first with what the later slot held the round before, and again
+    with that slot's new rows: values of the earlier chunk below 2^-6 of the old rows' scale keep
+    fewer bits.  (Runs of chunks of 15 tokens or more share no block with one another.)
     """
 
     def __init__(self, window: RollingWindow, heads: int, head_dim: int, num_layers: int = 1,
                  device="cuda", page_tables: Optional[torch.Tensor] = None,
-                 fill: Optional[float] = None, fp8_block: bool = False):
+                 fill: Optional[float] = None, fp8_block: bool = False, append_runs: bool = False):
         from .layer import PagedPool, PagedPoolFp8Block
         self.window = window
         self.num_layers = int(num_layers)
         self.fp8_block = bool(fp8_block)
+        self.append_runs = bool(append_runs)
+        if self.append_runs and not self.fp8_block:
+            raise ValueError("append_runs is for an FP8 cache: a bf16 cache's rows share no scale")
         if self.fp8_block:
             if fill is not None:
                 raise ValueError("an FP8 cache starts out zeroed: no fill")
@@ -248,17 +257,22 @@ class RollingCache:
         from .layer import _scratch
         L = self.window.chunk_len
 
-        def append(slot, i):
-            rows = slice(i * L, (i + 1) * L)
-            args = (slot, slot + 1, k[rows], v[rows], rule,
+        def append(slot, i, chunks=1):
+            rows = slice(i * L, (i + chunks) * L)
+            args = (slot, slot + chunks, k[rows], v[rows], rule,
                     None if positions is None else positions[rows], k_weight, stream)
             if self.fp8_block:
                 lay.append(*args)
             else:
                 lay.append_rope(*args)
         slots = view.query_rows_slots if self.window.copy_free else view.query_slots
-        for i, slot in enumerate(slots):
-            append(slot, i)
+        i = 0
+        while i < len(slots):
+            n = 1
+            while self.append_runs and i + n < len(slots) and slots[i + n] == slots[i] + n:
+                n += 1
+            append(slots[i], i, n)
+            i += n
         seg = None
         if self.window.copy_free:
             rows_end, kv_end = view.segments()
