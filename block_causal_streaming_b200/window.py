@@ -231,6 +231,8 @@ class RollingCache:
         rows of the round's query chunks in logical order (store pass, then in flight).  With
         ``rule`` (a :class:`NormRope`) the keys are normed and rotated on their way into the cache;
         ``positions``: int32 [T_q, axes], of the same rows."""
+        if rule is None and (positions is not None or k_weight is not None):
+            raise ValueError("positions and k_weight belong to a rule, and none is given")
         if view.t_q == 0:
             return
         lay = self.layer_view(view, layer)

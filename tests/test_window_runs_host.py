@@ -68,3 +68,19 @@ def test_append_runs_is_for_the_fp8_cache():
     with pytest.raises(ValueError, match="append_runs"):
         RollingCache(win, H, D, 1, "cpu", append_runs=True)
     RollingCache(win, H, D, 1, "cpu", fp8_block=True, append_runs=True)
+
+
+@pytest.mark.parametrize("copy_free", [False, True])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_positions_and_weights_without_a_rule_are_refused(fake, fp8, copy_free):
+    """They would be left out: the keys would go into the cache neither normed nor turned."""
+    win = RollingWindow(L, [1000, 500], 2, 16, copy_free=copy_free)
+    cache = RollingCache(win, H, D, 1, "cpu", fp8_block=fp8)
+    view = win.view(6)
+    n = L * len(view.query_rows_slots)
+    x = _bf(n, H, D)
+    for kw in (dict(positions=torch.zeros(n, 1, dtype=torch.int32)), dict(k_weight=_bf(D)),
+               dict(positions=torch.zeros(n, 1, dtype=torch.int32), k_weight=_bf(D))):
+        with pytest.raises(ValueError, match="rule"):
+            cache.run_layer(view, 0, x, x.clone(), x.clone(), x.clone(), **kw)
+    assert fake.appends == []
