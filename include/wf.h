@@ -580,9 +580,14 @@ int wf_kv_append_fp8_block(const wf_kv_pool_fp8_block_t* pool, int layer, int ch
  *   segments        as in wf_attn_forward_segments, except that a limit may also be 0 (the rows see
  *                   no key: out 0, lse -inf) and limits may come in any order.
  *   out             device bf16, laid out as q: softmax(scale q K^T) V over the rows' keys, on the
- *                   values the cache stands for.  Statistics, sums and accumulation are fp32; the
- *                   weights go into P.V with 11 bits down to 2^-27 of the row's largest and in steps
- *                   of 2^-37 of it below.
+ *                   values the cache stands for.  Statistics, sums and accumulation are fp32.  Weights
+ *                   and values go into P.V as f16 under powers of two: a weight times its value keeps
+ *                   11 bits down to a floor that the row's largest weight and the largest visible value
+ *                   V of its K/V head set, whether or not that value itself has any weight.  With n
+ *                   visible keys of weights p_j, and logits of scale sum |q||k| <= L,
+ *                     |out - exact| <= 2^-8 |exact| + (2^-10 + 2^-18 L) sum p_j |v_j| + n 2^-36 V:
+ *                   beside values 2^20 times as large nothing is lost in bf16, beside 2^30 times as
+ *                   large about 7 bits are left, beside 2^40 times as large none.
  *   lse_or_null     device fp32 [num_q_heads][rows] (optional).
  *   splits          1: no row's keys are cut (no workspace).  0: the library cuts them so that the
  *                   SMs are filled, and joins the parts in a second launch.  S > 1: with up to 32
