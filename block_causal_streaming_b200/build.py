@@ -9,6 +9,7 @@ the driver at run time:
 """
 from __future__ import annotations
 
+import glob
 import os
 import re
 import subprocess
@@ -19,12 +20,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libwf_b200.so")
 SOURCES = [os.path.join(CSRC, "wf_api.cu"), os.path.join(CSRC, "wf_window.cpp")]
-DEPENDS = SOURCES + [os.path.join(CSRC, f) for f in ("sm100.cuh", "attn_kernel.cuh",
-                                                      "append_kernel.cuh", "combine_kernel.cuh",
-                                                      "fp8_kernel.cuh", "norm_rope_kernel.cuh",
-                                                      "fp8_block_kernel.cuh", "attn_fp8_few_kernel.cuh",
-                                                      "attn_fp8_kernel.cuh",
-                                                      "publish_kernel.cuh")] + \
+DEPENDS = SOURCES + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + \
     [os.path.join(ROOT, "include", "wf.h")]
 
 NVCC_FLAGS = [
