@@ -480,7 +480,9 @@ int wf_attn_forward_e4m3(const wf_qk_e4m3_t* qk, const wf_kv_pool_t* kv_pages,
  * For one (token, head) row x of D values:
  *   y = x / sqrt(mean(x^2) + eps) * weight      (norm = 1; y = x with norm = 0)
  *   pair i turns by its angle:  (y_a, y_b) <- (y_a cos - y_b sin, y_a sin + y_b cos)
- * in fp32 throughout, rounded once.  Pairs are (2i, 2i + 1) with interleaved = 1, (i, pairs + i)
+ * in fp32 throughout, rounded once.  The mean is over the D values of one head (a layer that norms all
+ * heads of a token together runs that norm first and passes norm = 0); its sum of squares has to fit
+ * fp32, so magnitudes go up to 2^60 (and, with eps = 0, down to 2^-60).  Pairs are (2i, 2i + 1) with interleaved = 1, (i, pairs + i)
  * with 0; channels from 2 pairs on are not turned.  cos and sin are read from `cos_sin` at row
  * positions[token][axis of the pair]: the first axis_pairs[0] pairs turn with axis 0, the next
  * axis_pairs[1] with axis 1, and so on (one axis for a sequence; frame, row and column for video).
@@ -561,7 +563,7 @@ typedef struct {
  * written yet stand for 0.  A block whose page is outside the pool, or with a new token whose
  * position is outside the table, is not written (WF_ERR_PAGE_OOB, WF_ERR_POSITION).
  * Arguments and other errors as wf_kv_append_rope.  Calls that touch the same block must be
- * ordered (one stream).
+ * ordered (one stream), and the range's pages must differ from one another.
  */
 int wf_kv_append_fp8_block(const wf_kv_pool_fp8_block_t* pool, int layer, int chunk_begin,
                            int chunk_end, const void* k, int64_t k_stride, const void* v,
@@ -596,6 +598,8 @@ int wf_kv_append_fp8_block(const wf_kv_pool_fp8_block_t* pool, int layer, int ch
  *   workspace       device memory, 16-byte aligned, wf_attn_fp8_block_workspace_size bytes for the
  *                   same arguments; may be null when that is 0.  Not shared by calls, or captured
  *                   graphs, that may run at the same time.
+ * Logits have to fit fp32; a query row with an infinite or NaN value is NaN.  out may be q itself; no
+ * other overlap.
  * A page outside the pool is read as page 0 and recorded (WF_ERR_PAGE_OOB).  Errors:
  * WF_ERR_INVALID_ARG for null or misaligned pointers, scale <= 0, splits < 0; WF_ERR_SHAPE for
  * segments or head counts that break the rules; WF_ERR_CAPACITY when num_keys needs more than
