@@ -1670,6 +1670,9 @@ namespace {
 
 constexpr int kMaxFp8Splits = 256;
 
+// Keys of a call: the kernels count tokens in 32 bits and look up to 2048 past the last one.
+constexpr int kMaxKeys = INT32_MAX - 4096;
+
 // The non-empty segments of a call: rows [row_end[i-1], row_end[i]) see keys [0, kv[i]).
 struct SegmentList {
   int n = 0, t_q = 0, max_kv = 0;
@@ -1680,7 +1683,8 @@ struct SegmentList {
 int segment_list(const wf_segments_t* seg, SegmentList* out) {
   if (seg == nullptr || seg->rows_end == nullptr || seg->kv_end == nullptr)
     return WF_ERR_INVALID_ARG;
-  if (seg->num_segments < 1 || seg->num_segments > WF_MAX_CHUNKS || seg->num_keys < 0)
+  if (seg->num_segments < 1 || seg->num_segments > WF_MAX_CHUNKS || seg->num_keys < 0 ||
+      seg->num_keys > kMaxKeys)
     return WF_ERR_SHAPE;
   int prev = 0;
   for (int i = 0; i < seg->num_segments; ++i) {

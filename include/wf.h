@@ -580,7 +580,8 @@ int wf_kv_append_fp8_block(const wf_kv_pool_fp8_block_t* pool, int layer, int ch
  *   kv_pages        the FP8 cache; every key below the largest kv_end must have been appended.  Rows
  *                   past it may hold anything, NaN included.
  *   segments        as in wf_attn_forward_segments, except that a limit may also be 0 (the rows see
- *                   no key: out 0, lse -inf) and limits may come in any order.
+ *                   no key: out 0, lse -inf), limits may come in any order, and num_keys is at most
+ *                   2^31 - 4097.
  *   out             device bf16, laid out as q: softmax(scale q K^T) V over the rows' keys, on the
  *                   values the cache stands for.  Statistics, sums and accumulation are fp32.  Weights
  *                   and values go into P.V as f16 under powers of two: a weight times its value keeps
