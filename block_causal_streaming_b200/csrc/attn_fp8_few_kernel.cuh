@@ -29,9 +29,11 @@
 // bytes are.  The warps' results are joined in shared memory, the parts of a split key range by
 // wf_join_kernel.
 //
-// Bound by HBM.  One token, 40 heads x 51 480 keys (527 MB): 89 us, 5.9 TB/s, 0.90 of a copy.  One
-// token of 32 heads on 8 x 37 441 keys (77 MB): 17 to 20 us in a graph, 4.1 TB/s; of these about 12 are
-// the bytes, the rest the first page-table and scale look-ups, the last blocks and the join.  On the way
+// One row is bound by HBM.  One token, 40 heads x 51 480 keys (527 MB): 88-92 us, 5.8-6.0 TB/s, 0.88-0.91
+// of a copy.  One token of 32 heads on 8 x 37 441 keys (77 MB): 20 us in a graph, 3.8 TB/s; of these about
+// 12 are the bytes, the rest the first page-table and scale look-ups, the last blocks and the join.  More
+// rows are bound by latency: a warp has one block of 16 keys in work at a time, and above 16 rows an SM
+// has 8 warps: 12 heads x 37 440 keys, 1 row 25.6 us, 8 rows 27.5, 16 rows 35.4, 32 rows 49.5.  On the way
 // there: codes straight to registers 38 us (130 with 40 heads), one TMA ring for a CTA 29 (109), a ring
 // for each warp 28 (111), keys as the rows of the products instead of query rows, so that no shuffle
 // is needed between them, 23 (93), launches over the tail of the kernel before 21 (89).

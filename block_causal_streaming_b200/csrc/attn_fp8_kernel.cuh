@@ -34,12 +34,14 @@
 // SMs: 1.54 units each, where whole units take 2 turns and uniform parts 4 to 5 percent of joining
 // and 10 of idle SMs), and loads run ahead from one piece into the next.
 //
-// Bound by the exponentials (MUFU) and the tensor pipe together, both three quarters busy, in a chain
-// that passes one S buffer between two Q tiles, and in long runs by the power limit.  12 heads of 128:
-// the 5-chunk wavefront (23 400 rows, up to 32 760 keys, 3.36 TFLOP) 2.70-2.79 ms for a single call,
-// 3.05 in a loop at about 1.64 GHz (0.73 and 0.66 of a cuBLAS bf16 product; the bf16 kernel takes 2.99 in
-// the same loop); one chunk of 4680 rows against 37 440 keys 850-910 us in a few calls, 0.98 ms in a loop.
-// A pair of Q tiles takes 3240 cycles for a key tile, with 54 % of the issue slots busy.
+// Bound by the chain that passes one S buffer between two Q tiles, no pipe in it full: MUFU 63 %, tensor
+// pipe 61 %, issue slots 51 % (one chunk, counters); a pair of Q tiles takes 3240 cycles for a key tile,
+// of which either pipe is busy for about 2048.  In long runs by the power limit too.  12 heads of 128: the
+// 5-chunk wavefront (23 400 rows, up to 32 760 keys, 3.36 TFLOP) 3.00-3.12 ms call after call, 0.65 of a
+// cuBLAS bf16 product (2.8 for the fastest single ones; the bf16 kernel takes 2.99 in the same loop); one
+// chunk of 4680 rows against 37 440 keys 0.98-1.0 ms call after call, 860-910 us for a few; 12 heads of 64
+// 763 us.  With no more than 128 packed rows a unit has one Q tile, half the softmax warps idle and the
+// chain is serial: 128 rows of 12 heads 56 us (DRAM 17), MUFU and tensor pipe under 30 %.
 // Steps on the way (the wavefront unless said otherwise): row sums with packed adds 3.50 -> 3.11 ms;
 // pieces instead of uniform parts, one chunk 1000 -> 854 us; loops that fit the instruction cache
 // (compact waits, one piece loop for the eight warps that are not softmax) were worth a factor 1.7.

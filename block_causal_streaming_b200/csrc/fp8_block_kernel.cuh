@@ -23,9 +23,10 @@
 // of V alternate, and at any time half the warp pairs work on K, so that arithmetic (K) and plain
 // copying (V) share the SM.
 //
-// On 23 400 tokens of 12 heads of 128, 3 axes: 50.6 us, 216 MB, 4.3 TB/s; 51.4 with all K before all V,
+// On 23 400 tokens of 12 heads of 128, 3 axes: 50.6 us, 216 MB, 4.3 TB/s (one chunk of 4680: 10.0 us);
+// 51.4 with all K before all V,
 // 65 with one warp for all 16 rows (64 values a lane).  Bound by how loads and arithmetic overlap: the
-// issue slots are half full and HBM is at 0.65 of a copy.  Neither more warps (3 CTAs an SM: 53.1) nor
+// issue slots are at 41 % and HBM at 0.65 of a copy.  Neither more warps (3 CTAs an SM: 53.1) nor
 // more heads asked for ahead (2 through shared memory 53.1, 3 54.9, 5 62.9) nor 4 warps to a block
 // (55.7) did better.
 #pragma once

@@ -281,8 +281,9 @@ __device__ __forceinline__ void load_weight(const __nv_bfloat16* weight, int64_t
 // set 1 (values) is copied bit for bit.
 //
 // Bound by HBM: 4 D bytes for each row, and the table from L2.  23 400 tokens, 12 + 12 heads of 128 with
-// three axes: 52.3 us, 5.5 TB/s (0.84 of a copy); the same into pages, 52.2.  With 8-byte loads 79 us;
-// with single floats instead of packed pairs 57 (issue slots two thirds full).
+// three axes: 52.5 us in a graph, 5.5 TB/s (0.84 of a copy), 55-57 call after call (0.77-0.80); the same into
+// pages, 52.3 and 53-55.  With 8-byte loads 79 us; with single floats instead of packed pairs 57 (issue
+// slots two thirds full).
 template <int D, int kMode, bool kAppend>
 __global__ void __launch_bounds__(kNormRopeThreads, kNormRopeCtas)
     wf_norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
